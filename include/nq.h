@@ -69,7 +69,9 @@ typedef enum nq_status {
     NQ_ERR_DEVICE = 5,    /* current device is not compute capability 10.0 (B200) */
     NQ_ERR_LAUNCH = 6,    /* a kernel launch failed */
     NQ_ERR_TIMEOUT = 7,   /* a bounded device-side wait gave up (seen by nq_sync_status) */
-    NQ_ERR_SCRATCH_LIMIT = 8 /* nq_lrb_matvec_noalloc: the call needs more than NQ_NOALLOC_SCRATCH_BYTES */
+    NQ_ERR_SCRATCH_LIMIT = 8, /* nq_lrb_matvec_noalloc: the call needs more than NQ_NOALLOC_SCRATCH_BYTES */
+    NQ_ERR_VALUE = 9,     /* a scalar argument is outside its range */
+    NQ_ERR_INDEX = 10     /* a row list held an index outside its range (seen by nq_sync_status) */
 } nq_status;
 
 /* One LRB linear layer.  All pointers are device pointers; the struct itself is host
@@ -265,8 +267,126 @@ NQ_API nq_status nq_mlp_gate_up(const nq_lrb_layer* gate, const nq_lrb_layer* up
 NQ_API nq_status nq_silu_mul(const uint16_t* g, const uint16_t* u, uint16_t* h, int64_t n, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection.  The pages freeze the binary
+ * factors; what a served or tuned model adds per request or per tenant is a low-rank term on the
+ * projection's output, y'[m] = y[m] + scale_a B_a A_a x[m] for the adapter a of row m.  The
+ * pages have no counterpart to these entry points.
+ *
+ * n adapters of one projection, all of one rank (lower ranks are padded with zero rows of A or
+ * zero columns of B).  1 <= n <= NQ_ADAPTER_MAX_N, 1 <= rank <= NQ_ADAPTER_MAX_RANK.
+ * Fastest where d_in, d_out, rank, lda and ldb are multiples of 8; any value works.
+ */
+#define NQ_ADAPTER_MAX_RANK 128
+#define NQ_ADAPTER_MAX_N 16384
+typedef struct nq_adapters {
+    int64_t n;           /* adapters */
+    int64_t rank;
+    int64_t d_in;        /* input features of the projection */
+    int64_t d_out;       /* output features of the projection */
+    const uint16_t* A;   /* [n][rank][lda] bf16, columns 0..d_in-1 are read */
+    int64_t lda;         /* >= d_in */
+    const uint16_t* B;   /* [n][d_out][ldb] bf16, columns 0..rank-1 are read */
+    int64_t ldb;         /* >= rank */
+    const float* scale;  /* [n] fp32, or NULL (all 1) */
+} nq_adapters;
+
+/*
+ * nq_adapter_rows -- the rows of a batch grouped by adapter, once for all projections of a step.
+ *   ids [M] int32: the adapter of each row; any value outside 0..n-1 means that the row has none.
+ *   rows [M] int32: the row numbers, adapter 0's first, each group in ascending order, the rows
+ *   without an adapter last; offsets [n + 1] int32: adapter a has rows[offsets[a] ..
+ *   offsets[a+1]), and rows[offsets[n] .. M) have none.
+ * A caller that knows its batch on the host may fill both lists itself.  1 <= M < 2^31.
+ */
+NQ_API nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32_t* rows, int32_t* offsets,
+                                 void* stream);
+
+/*
+ * nq_adapter_forward -- for every row m with adapter a:
+ *     t[m] = scale_a A_a x[m],   out[m] = bf16( y[m] + B_a t[m] );
+ * a row without an adapter gets out[m] = y[m] and t[m] = 0, and its x[m] is not read.
+ *   x [M][d_in], y and out [M][d_out] bf16; out may be y.  t [M][rank] fp32, or NULL: what
+ *   nq_adapter_backward takes.  rows, offsets: as nq_adapter_rows writes them.  Each row must be
+ *   listed once: a row that is not listed is left as it was, and a row listed more than once is
+ *   left undefined.  A list entry outside 0..M-1 or offsets out of order are skipped and make the
+ *   next nq_sync_status return NQ_ERR_INDEX; no memory outside the arguments is touched.
+ * Sums are fp32 in a fixed order (run-to-run identical); out is rounded once.  Needs no workspace.
+ */
+NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets,
+                                    const uint16_t* x, const uint16_t* y, uint16_t* out, float* t, int64_t M,
+                                    void* stream);
+
+/*
+ * nq_adapter_backward -- for L = sum_m <ybar[m], out[m]>, with u[m] = scale_a B_a^T ybar[m]:
+ *     xbar_out[m] = bf16( xbar[m] + A_a^T u[m] )
+ *     gA_a = dL/dA_a = sum over a's rows of u[m] x[m]^T        [n][rank][d_in] bf16, contiguous
+ *     gB_a = dL/dB_a = sum over a's rows of ybar[m] t[m]^T     [n][d_out][rank] bf16, contiguous
+ *   xbar [M][d_in] bf16: the gradient that the shared projection carries back (nq_lrb_transposed);
+ *   xbar_out may be xbar.  t: as nq_adapter_forward wrote it (it includes the scale).  gA and gB
+ *   are written whole, zeros for an adapter without rows.  xbar_out (then xbar too), gA and gB
+ *   may each be NULL; t is needed for gB, x for gA.
+ * Sums are fp32 in a fixed order; every output is rounded once to bf16.  Where tensor cores are
+ * used (widths in multiples of 8), t and u enter the second products as the sum of two bf16
+ * values, which keeps 16 of their bits.  ws: nq_adapter_workspace_bytes(S, M) bytes (0 for invalid
+ * adapters or M).
+ */
+NQ_API size_t nq_adapter_workspace_bytes(const nq_adapters* S, int64_t M);
+NQ_API nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets,
+                                     const uint16_t* x, const uint16_t* ybar, const float* t, const uint16_t* xbar,
+                                     uint16_t* xbar_out, uint16_t* gA, uint16_t* gB, int64_t M, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * The norms between two blocks of a decoder made of LRB projections, with the gate and the
+ * residual (the pages quantise the projections only).  For a block's output y and the residual
+ * stream h, q(v) = sqrt(mean_j v_j^2 + eps) per row, w' = w_offset + w:
+ *     z     = w_post' (.) y / q(y)  where post_norm, else z = y
+ *     h_out = alpha h + gate (.) z          (y NULL: h_out = alpha h)
+ *     x     = w_pre' (.) h_out / q(h_out)   (of the unrounded h_out)
+ */
+typedef struct nq_block_norm {
+    int64_t d;              /* channels, 1 <= d <= NQ_BLOCK_NORM_MAX_D */
+    const uint16_t* w_pre;  /* [d] bf16, or NULL: w_pre' = 1 */
+    const uint16_t* w_post; /* [d] bf16, or NULL: w_post' = 1 */
+    float w_offset;         /* added to the weights (1 for weights stored as w - 1) */
+    float alpha;            /* residual scale */
+    float eps;              /* > 0 */
+    int32_t post_norm;      /* 0 or 1 */
+    int32_t h_f32;          /* the residual stream is fp32 (1) or bf16 (0) */
+} nq_block_norm;
+#define NQ_BLOCK_NORM_MAX_D 1048576
+
+/*
+ * nq_block_norm_forward.  y [M][d] bf16 or NULL; h, h_out [M][d] bf16 or fp32 (h_f32); x [M][d]
+ * bf16.  gate: bf16, row m at gate + m ld_gate, ld_gate >= d (a gate per row) or 0 (one vector
+ * for all rows); NULL: no gate (ones).  One of h_out and x may be NULL.  h_out may be h and x
+ * may be y; other overlaps are undefined.  Finite results need sums of squares within fp32.
+ * 1 <= M < 2^31.
+ */
+NQ_API nq_status nq_block_norm_forward(const nq_block_norm* N, const uint16_t* y, const void* h, const uint16_t* gate,
+                                       int64_t ld_gate, void* h_out, uint16_t* x, int64_t M, void* stream);
+
+/*
+ * nq_block_norm_backward -- with gh_out = dL/dh_out (as h_out is used further on) and gx = dL/dx:
+ *   gh [M][d] = dL/dh (h's type), gy [M][d] = dL/dy bf16, g_w_pre and g_w_post [d] fp32 (summed over
+ *   the rows), g_gate: fp32 [d] for one shared gate (ld_gate 0), bf16 [M][d] for a gate per row.
+ * y, gate: as in the forward call; h_out: what it wrote (its norm is taken again from it).  gx NULL
+ * or gh_out NULL: zero.  Every output may be NULL; those that need y, the gate or post_norm are
+ * refused without them (NQ_ERR_NULL; g_w_post without post_norm: NQ_ERR_VALUE).  gh may be gh_out
+ * and gy may be gx.  Row gradients are rounded once from fp32; the sums over rows are fp32 within
+ * a block of rows and fp64 across blocks, in a fixed order.
+ * ws: nq_block_norm_workspace_bytes(N, M) bytes (0 for invalid parameters).
+ */
+NQ_API size_t nq_block_norm_workspace_bytes(const nq_block_norm* N, int64_t M);
+NQ_API nq_status nq_block_norm_backward(const nq_block_norm* N, const uint16_t* y, const void* h_out,
+                                        const uint16_t* gate, int64_t ld_gate, const uint16_t* gx, const void* gh_out,
+                                        void* gh, uint16_t* gy, float* g_w_pre, float* g_w_post, void* g_gate,
+                                        int64_t M, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * nq_sync_status -- synchronises `stream`, then reports and clears this device's error
  * word: NQ_ERR_TIMEOUT if a bounded device-side wait gave up since the last check,
+ * NQ_ERR_INDEX if a row list held an index outside its range (timeouts are reported first),
  * NQ_ERR_LAUNCH if the stream reported an asynchronous CUDA error, NQ_OK otherwise.
  */
 NQ_API nq_status nq_sync_status(void* stream);

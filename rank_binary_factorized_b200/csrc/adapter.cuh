@@ -1,0 +1,111 @@
+// adapter.cuh -- arguments and device helpers shared by the low-rank adapter kernels.
+#pragma once
+
+#include "nq_common.cuh"
+
+namespace nq {
+
+// One product pair of the adapters, forward or its transpose:
+//   t[m] = scale_a P_a z[m],  out[m] = base[m] + Q_a t[m],  a = the adapter of row m
+// forward: z = x, P = A, Q = B; backward: z = ybar, P = B^T, Q = A^T, t = u.
+struct AdapterArgs {
+    const int32_t* rows;     // [M] rows grouped by adapter, rows without one last
+    const int32_t* offsets;  // [n + 1] where each adapter's rows begin in `rows`
+    const uint16_t* z;       // [M][K] bf16
+    const uint16_t* base;    // [M][N] bf16
+    uint16_t* out;           // [M][N] bf16, may be base; nullptr: only t is wanted
+    float* t;                // [M][rank] fp32 or nullptr
+    const uint16_t* A;       // [n][rank][lda] bf16
+    const uint16_t* B;       // [n][d_out][ldb] bf16
+    const float* scale;      // [n] or nullptr (ones)
+    int64_t lda, ldb, d_in, d_out;
+    int64_t K, N;            // widths of z and of base
+    int64_t M;
+    int n, rank;
+    unsigned int* err;
+};
+
+// Sum over the tokens of each adapter (a = blockIdx.y):
+//   gA_a[r][j] = sum_m u[m][r] x[m][j],   gB_a[i][r] = sum_m ybar[m][i] t[m][r]
+struct AdapterGradArgs {
+    const int32_t* rows;
+    const int32_t* offsets;
+    const uint16_t* x;     // [M][d_in]
+    const uint16_t* ybar;  // [M][d_out]
+    const float* t;        // [M][rank]
+    const float* u;        // [M][rank]
+    uint16_t* gA;          // [n][rank][d_in] bf16 or nullptr
+    uint16_t* gB;          // [n][d_out][rank] bf16 or nullptr
+    int64_t d_in, d_out, M;
+    int n, rank;
+    unsigned int* err;
+};
+
+// A run of at most `rows_per_tile` entries of `rows` that share an adapter.
+struct AdapterTile {
+    int adapter;  // n: rows without an adapter; -1: no such tile
+    int first;    // index into rows
+    int count;
+};
+
+// Bounds of adapter a's entries in `rows`, forced into 0 <= first <= last <= M whatever the
+// offsets say; a == n: the rows after the last adapter's.  Offsets outside that order are
+// reported.
+__device__ __forceinline__ void adapter_bounds(const int32_t* offsets, int n, int64_t M, int a, int& first, int& last,
+                                               unsigned int* err) {
+    const int64_t lo = offsets[a], hi = a < n ? static_cast<int64_t>(offsets[a + 1]) : M;
+    const bool ok = lo >= 0 && lo <= hi && hi <= M && (a > 0 || lo == 0);
+    if (!ok) flag_error(err, kErrIndex);
+    first = static_cast<int>(ok ? lo : 0);
+    last = static_cast<int>(ok ? hi : 0);
+}
+
+// Tile number `tile` when every group's rows are cut into tiles of rows_per_tile, groups in
+// order.  A whole warp calls it; 32 groups are scanned at a time.
+__device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, int64_t M, int rows_per_tile, int tile,
+                                                 unsigned int* err) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;  // tiles of the groups before this batch of 32
+    for (int a0 = 0; a0 <= n; a0 += 32) {
+        const int a = a0 + lane;
+        int first = 0, last = 0;
+        if (a <= n) adapter_bounds(offsets, n, M, a, first, last, err);
+        const int mine = (last - first + rows_per_tile - 1) / rows_per_tile;
+        int upto = mine;  // inclusive sum over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int local = tile - before;
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, local < upto);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            AdapterTile t;
+            t.adapter = a0 + src;
+            const int off = (local - (__shfl_sync(0xFFFFFFFFu, upto, src) - __shfl_sync(0xFFFFFFFFu, mine, src))) *
+                            rows_per_tile;
+            t.first = __shfl_sync(0xFFFFFFFFu, first, src) + off;
+            t.count = min(rows_per_tile, __shfl_sync(0xFFFFFFFFu, last, src) - t.first);
+            return t;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    return {-1, 0, 0};
+}
+
+// Upper bound of the number of tiles for any grouping of M rows into n adapters and "none".
+inline int64_t max_adapter_tiles(int64_t M, int64_t n, int rows_per_tile) {
+    const int64_t groups = n + 1 < M ? n + 1 : M;
+    return (M - groups) / rows_per_tile + groups;
+}
+
+// Entry i of `rows`, or -1 (reported) when it is not a row.
+__device__ __forceinline__ int checked_row(const int32_t* rows, int64_t i, int64_t M, unsigned int* err) {
+    const int r = rows[i];
+    if (r >= 0 && r < M) return r;
+    flag_error(err, kErrIndex);
+    return -1;
+}
+
+}  // namespace nq

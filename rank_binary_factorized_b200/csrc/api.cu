@@ -2,8 +2,11 @@
 // workspace planning and dispatch to the kernels.  No allocation, no synchronisation (except
 // nq_sync_status), no fallback: a device that is not sm_100 gets NQ_ERR_DEVICE.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
+#include "adapter.cuh"
+#include "norm.cuh"
 #include "nq_common.cuh"
 
 namespace nq {
@@ -27,6 +30,10 @@ size_t nq_sign_grads_ws(const nq_lrb_layer* L, const nq_lrb_layer* X, int64_t M)
 nq_status nq_launch_sign_grads(const nq_lrb_layer* L, const nq_lrb_layer* X, const uint16_t* x, const uint16_t* ybar,
                                int64_t M, float* gU, int64_t ldgu, float* gV, int64_t ldgv, void* ws,
                                cudaStream_t stream, bool pdl);
+nq_status nq_launch_adapter_rows(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl);
+nq_status nq_launch_adapter_grad_any(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl);
+nq_status nq_launch_adapter_group_rows(const int32_t* ids, int64_t M, int n, int32_t* rows, int32_t* offsets,
+                                       cudaStream_t stream, bool pdl);
 
 namespace {
 
@@ -188,6 +195,8 @@ const char* nq_status_string(nq_status s) {
         case NQ_ERR_TIMEOUT: return "NQ_ERR_TIMEOUT: a bounded device-side wait gave up";
         case NQ_ERR_SCRATCH_LIMIT:
             return "NQ_ERR_SCRATCH_LIMIT: the call needs more scratch than nq_lrb_matvec_noalloc's static array";
+        case NQ_ERR_VALUE: return "NQ_ERR_VALUE: a scalar argument is outside its range";
+        case NQ_ERR_INDEX: return "NQ_ERR_INDEX: a row list held an index outside its range";
     }
     return "unknown nq_status";
 }
@@ -422,6 +431,215 @@ nq_status nq_silu_mul(const uint16_t* g, const uint16_t* u, uint16_t* h, int64_t
     return nq_launch_silu_mul(g, u, h, n, static_cast<cudaStream_t>(stream), pdl_enabled());
 }
 
+// ------------------------------------------------------------------ low-rank adapters
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+
+nq_status check_adapters(const nq_adapters* S, int64_t M) {
+    if (!S || !S->A || !S->B) return NQ_ERR_NULL;
+    if (S->n < 1 || S->n > NQ_ADAPTER_MAX_N || S->rank < 1 || S->rank > NQ_ADAPTER_MAX_RANK) return NQ_ERR_SHAPE;
+    if (S->d_in < 1 || S->d_out < 1 || S->d_in > kMaxRows || S->d_out > kMaxRows || S->lda < S->d_in ||
+        S->ldb < S->rank)
+        return NQ_ERR_SHAPE;
+    if (M < 1 || M > kMaxRows) return NQ_ERR_SHAPE;
+    if (!aligned16(S->A) || !aligned16(S->B) || (S->scale && !aligned16(S->scale))) return NQ_ERR_ALIGN;
+    return NQ_OK;
+}
+
+// Workspace: u [M][rank] fp32 of the backward pass.
+size_t adapter_ws(const nq_adapters* S, int64_t M) {
+    return NQ_WS_HEADER_BYTES + (static_cast<size_t>(M) * S->rank * sizeof(float) + 255) / 256 * 256;
+}
+
+nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const int32_t* offsets, int64_t M) {
+    nq::AdapterArgs a{};
+    a.rows = rows;
+    a.offsets = offsets;
+    a.A = S->A;
+    a.B = S->B;
+    a.scale = S->scale;
+    a.lda = S->lda;
+    a.ldb = S->ldb;
+    a.d_in = S->d_in;
+    a.d_out = S->d_out;
+    a.M = M;
+    a.n = static_cast<int>(S->n);
+    a.rank = static_cast<int>(S->rank);
+    a.err = nq_host::error_word();
+    return a;
+}
+
+}  // namespace
+
+nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32_t* rows, int32_t* offsets, void* stream) {
+    if (M < 1 || M > kMaxRows || n < 1 || n > NQ_ADAPTER_MAX_N) return NQ_ERR_SHAPE;
+    if (!ids || !rows || !offsets) return NQ_ERR_NULL;
+    if (!aligned16(ids) || !aligned16(rows) || !aligned16(offsets)) return NQ_ERR_ALIGN;
+    DeviceInfo* d = current_device();
+    if (!d || !d->ok) return NQ_ERR_DEVICE;
+    return nq_launch_adapter_group_rows(ids, M, static_cast<int>(n), rows, offsets, static_cast<cudaStream_t>(stream),
+                                        pdl_enabled());
+}
+
+size_t nq_adapter_workspace_bytes(const nq_adapters* S, int64_t M) {
+    return check_adapters(S, M) == NQ_OK ? adapter_ws(S, M) : 0;
+}
+
+nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets, const uint16_t* x,
+                             const uint16_t* y, uint16_t* out, float* t, int64_t M, void* stream) {
+    nq_status st = check_adapters(S, M);
+    if (st != NQ_OK) return st;
+    if (!rows || !offsets || !x || !y || !out) return NQ_ERR_NULL;
+    if (!aligned16(rows) || !aligned16(offsets) || !aligned16(x) || !aligned16(y) || !aligned16(out) ||
+        (t && !aligned16(t)))
+        return NQ_ERR_ALIGN;
+    DeviceInfo* d = current_device();
+    if (!d || !d->ok) return NQ_ERR_DEVICE;
+    nq::AdapterArgs a = adapter_args(S, rows, offsets, M);
+    a.z = x;
+    a.base = y;
+    a.out = out;
+    a.t = t;
+    a.K = S->d_in;
+    a.N = S->d_out;
+    return nq_launch_adapter_rows(a, false, static_cast<cudaStream_t>(stream), pdl_enabled());
+}
+
+nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets, const uint16_t* x,
+                              const uint16_t* ybar, const float* t, const uint16_t* xbar, uint16_t* xbar_out,
+                              uint16_t* gA, uint16_t* gB, int64_t M, void* ws, size_t ws_bytes, void* stream) {
+    nq_status st = check_adapters(S, M);
+    if (st != NQ_OK) return st;
+    if (!rows || !offsets || !ybar || !ws || (xbar_out && !xbar) || (gA && !x) || (gB && !t)) return NQ_ERR_NULL;
+    const void* ptrs[] = {rows, offsets, x, ybar, t, xbar, xbar_out, gA, gB, ws};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return NQ_ERR_ALIGN;
+    if (ws_bytes < adapter_ws(S, M)) return NQ_ERR_WORKSPACE;
+    DeviceInfo* d = current_device();
+    if (!d || !d->ok) return NQ_ERR_DEVICE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* u = reinterpret_cast<float*>(static_cast<char*>(ws) + NQ_WS_HEADER_BYTES);
+    if (xbar_out || gA) {
+        nq::AdapterArgs a = adapter_args(S, rows, offsets, M);
+        a.z = ybar;
+        a.base = xbar;
+        a.out = xbar_out;
+        a.t = gA ? u : nullptr;
+        a.K = S->d_out;
+        a.N = S->d_in;
+        if ((st = nq_launch_adapter_rows(a, true, s, pdl_enabled())) != NQ_OK) return st;
+    }
+    if (!gA && !gB) return NQ_OK;
+    nq::AdapterGradArgs g{};
+    g.rows = rows;
+    g.offsets = offsets;
+    g.x = x;
+    g.ybar = ybar;
+    g.t = t;
+    g.u = u;
+    g.gA = gA;
+    g.gB = gB;
+    g.d_in = S->d_in;
+    g.d_out = S->d_out;
+    g.M = M;
+    g.n = static_cast<int>(S->n);
+    g.rank = static_cast<int>(S->rank);
+    g.err = nq_host::error_word();
+    return nq_launch_adapter_grad_any(g, s, pdl_enabled());
+}
+
+// ------------------------------------------------------------------ norms between blocks
+namespace {
+
+nq_status check_block_norm(const nq_block_norm* N, int64_t M) {
+    if (!N) return NQ_ERR_NULL;
+    if (N->d < 1 || N->d > NQ_BLOCK_NORM_MAX_D || M < 1 || M > kMaxRows) return NQ_ERR_SHAPE;
+    if ((N->w_pre && !aligned16(N->w_pre)) || (N->w_post && !aligned16(N->w_post))) return NQ_ERR_ALIGN;
+    if (!(N->eps > 0.f) || !std::isfinite(N->eps) || !std::isfinite(N->alpha) || !std::isfinite(N->w_offset) ||
+        (N->post_norm != 0 && N->post_norm != 1) || (N->h_f32 != 0 && N->h_f32 != 1))
+        return NQ_ERR_VALUE;
+    return NQ_OK;
+}
+
+nq_status check_gate(const nq_block_norm* N, const uint16_t* gate, int64_t ld_gate) {
+    return gate && ld_gate != 0 && ld_gate < N->d ? NQ_ERR_SHAPE : NQ_OK;
+}
+
+}  // namespace
+
+nq_status nq_block_norm_forward(const nq_block_norm* N, const uint16_t* y, const void* h, const uint16_t* gate,
+                                int64_t ld_gate, void* h_out, uint16_t* x, int64_t M, void* stream) {
+    nq_status st = check_block_norm(N, M);
+    if (st != NQ_OK) return st;
+    if (!h || (!h_out && !x)) return NQ_ERR_NULL;
+    if ((st = check_gate(N, gate, ld_gate)) != NQ_OK) return st;
+    const void* ptrs[] = {y, h, gate, h_out, x};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return NQ_ERR_ALIGN;
+    DeviceInfo* dev = current_device();
+    if (!dev || !dev->ok) return NQ_ERR_DEVICE;
+    nq::NormFwdArgs a{};
+    a.y = y;
+    a.h = h;
+    a.h_out = h_out;
+    a.x = x;
+    a.gate = y ? gate : nullptr;
+    a.ld_gate = ld_gate;
+    a.w_post = N->w_post;
+    a.w_pre = N->w_pre;
+    a.d = N->d;
+    a.alpha = N->alpha;
+    a.eps = N->eps;
+    a.w_offset = N->w_offset;
+    a.post = y && N->post_norm;
+    a.h_f32 = N->h_f32 != 0;
+    return nq_launch_block_norm(a, M, static_cast<cudaStream_t>(stream), pdl_enabled());
+}
+
+size_t nq_block_norm_workspace_bytes(const nq_block_norm* N, int64_t M) {
+    return check_block_norm(N, M) == NQ_OK ? nq_block_norm_grad_ws(N->d, M) : 0;
+}
+
+nq_status nq_block_norm_backward(const nq_block_norm* N, const uint16_t* y, const void* h_out, const uint16_t* gate,
+                                 int64_t ld_gate, const uint16_t* gx, const void* gh_out, void* gh, uint16_t* gy,
+                                 float* g_w_pre, float* g_w_post, void* g_gate, int64_t M, void* ws, size_t ws_bytes,
+                                 void* stream) {
+    nq_status st = check_block_norm(N, M);
+    if (st != NQ_OK) return st;
+    if (!h_out || !ws || (!y && (gy || g_w_post || g_gate)) || (!gate && g_gate)) return NQ_ERR_NULL;
+    if (g_w_post && !N->post_norm) return NQ_ERR_VALUE;
+    if ((st = check_gate(N, gate, ld_gate)) != NQ_OK) return st;
+    const void* ptrs[] = {y, h_out, gate, gx, gh_out, gh, gy, g_w_pre, g_w_post, g_gate, ws};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return NQ_ERR_ALIGN;
+    if (ws_bytes < nq_block_norm_grad_ws(N->d, M)) return NQ_ERR_WORKSPACE;
+    DeviceInfo* dev = current_device();
+    if (!dev || !dev->ok) return NQ_ERR_DEVICE;
+    const bool row_gate = gate && ld_gate != 0;
+    nq::NormBwdArgs a{};
+    a.y = y;
+    a.h_out = h_out;
+    a.gx = gx;
+    a.gh_out = gh_out;
+    a.gate = y ? gate : nullptr;
+    a.w_post = N->w_post;
+    a.w_pre = N->w_pre;
+    a.gh = gh;
+    a.gy = gy;
+    a.g_gate_rows = row_gate ? static_cast<uint16_t*>(g_gate) : nullptr;
+    a.M = M;
+    a.d = N->d;
+    a.ld_gate = ld_gate;
+    a.alpha = N->alpha;
+    a.eps = N->eps;
+    a.w_offset = N->w_offset;
+    a.post = y && N->post_norm;
+    a.h_f32 = N->h_f32 != 0;
+    return nq_launch_block_norm_grad(a, g_w_pre, g_w_post, row_gate ? nullptr : static_cast<float*>(g_gate), ws,
+                                     static_cast<cudaStream_t>(stream), pdl_enabled());
+}
+
 nq_status nq_sync_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return NQ_ERR_LAUNCH;
@@ -431,6 +649,7 @@ nq_status nq_sync_status(void* stream) {
         const unsigned int zero = 0u;
         cudaMemcpyToSymbol(nq::g_error_word, &zero, sizeof zero);
         if (word & nq::kErrTimeout) return NQ_ERR_TIMEOUT;
+        if (word & nq::kErrIndex) return NQ_ERR_INDEX;
     }
     return NQ_OK;
 }

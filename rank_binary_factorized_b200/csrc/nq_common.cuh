@@ -20,9 +20,10 @@
 namespace nq {
 
 // Device error word (one per device that loads the library, defined in api.cu; kernels get
-// its address as an argument).  Set with atomicOr by a kernel whose bounded wait gave up,
-// read and cleared by nq_sync_status.
+// its address as an argument).  Set with atomicOr by a kernel whose bounded wait gave up or
+// whose row list holds an index outside its range, read and cleared by nq_sync_status.
 constexpr unsigned int kErrTimeout = 1u;
+constexpr unsigned int kErrIndex = 2u;
 
 // Iteration cap for every spin-wait on device (each iteration sleeps ~128 ns with
 // __nanosleep after the first few polls; 2^22 polls is well over a second).

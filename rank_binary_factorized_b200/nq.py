@@ -29,7 +29,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 NQ_OK = 0
 STATUS_NAMES = {0: "NQ_OK", 1: "NQ_ERR_NULL", 2: "NQ_ERR_SHAPE", 3: "NQ_ERR_ALIGN", 4: "NQ_ERR_WORKSPACE",
-                5: "NQ_ERR_DEVICE", 6: "NQ_ERR_LAUNCH", 7: "NQ_ERR_TIMEOUT"}
+                5: "NQ_ERR_DEVICE", 6: "NQ_ERR_LAUNCH", 7: "NQ_ERR_TIMEOUT", 8: "NQ_ERR_SCRATCH_LIMIT",
+                9: "NQ_ERR_VALUE", 10: "NQ_ERR_INDEX"}
 MATVEC_MAX_M = 8
 
 _i64 = ctypes.c_int64
@@ -39,6 +40,16 @@ _p = ctypes.c_void_p
 class nq_lrb_layer(ctypes.Structure):
     _fields_ = [("d_out", _i64), ("d_in", _i64), ("r", _i64), ("U", _p), ("ldu", _i64), ("V", _p), ("ldv", _i64),
                 ("s1", _p), ("s2", _p)]
+
+
+class nq_adapters(ctypes.Structure):
+    _fields_ = [("n", _i64), ("rank", _i64), ("d_in", _i64), ("d_out", _i64), ("A", _p), ("lda", _i64), ("B", _p),
+                ("ldb", _i64), ("scale", _p)]
+
+
+class nq_block_norm(ctypes.Structure):
+    _fields_ = [("d", _i64), ("w_pre", _p), ("w_post", _p), ("w_offset", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("post_norm", ctypes.c_int32), ("h_f32", ctypes.c_int32)]
 
 
 _lib.nq_pack_signs.restype = ctypes.c_int
@@ -77,6 +88,22 @@ _lib.nq_lrb_sign_grads.argtypes = [ctypes.POINTER(nq_lrb_layer), _p, _p, _i64, _
                                    _p]
 _lib.nq_selftest_bounded_wait.restype = ctypes.c_int
 _lib.nq_selftest_bounded_wait.argtypes = [_i64, _p]
+_lib.nq_adapter_rows.restype = ctypes.c_int
+_lib.nq_adapter_rows.argtypes = [_p, _i64, _i64, _p, _p, _p]
+_lib.nq_adapter_workspace_bytes.restype = ctypes.c_size_t
+_lib.nq_adapter_workspace_bytes.argtypes = [ctypes.POINTER(nq_adapters), _i64]
+_lib.nq_adapter_forward.restype = ctypes.c_int
+_lib.nq_adapter_forward.argtypes = [ctypes.POINTER(nq_adapters), _p, _p, _p, _p, _p, _p, _i64, _p]
+_lib.nq_adapter_backward.restype = ctypes.c_int
+_lib.nq_adapter_backward.argtypes = [ctypes.POINTER(nq_adapters), _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p,
+                                     ctypes.c_size_t, _p]
+_lib.nq_block_norm_forward.restype = ctypes.c_int
+_lib.nq_block_norm_forward.argtypes = [ctypes.POINTER(nq_block_norm), _p, _p, _p, _i64, _p, _p, _i64, _p]
+_lib.nq_block_norm_workspace_bytes.restype = ctypes.c_size_t
+_lib.nq_block_norm_workspace_bytes.argtypes = [ctypes.POINTER(nq_block_norm), _i64]
+_lib.nq_block_norm_backward.restype = ctypes.c_int
+_lib.nq_block_norm_backward.argtypes = [ctypes.POINTER(nq_block_norm), _p, _p, _p, _i64, _p, _p, _p, _p, _p, _p, _p,
+                                        _i64, _p, ctypes.c_size_t, _p]
 _lib.nq_sync_status.argtypes = [_p]
 _lib.nq_status_string.restype = ctypes.c_char_p
 _lib.nq_status_string.argtypes = [ctypes.c_int]
@@ -250,8 +277,16 @@ def lrb_matmul(layer: Layer, x: torch.Tensor, y=None, ws=None, stream=None) -> t
     return _forward("nq_lrb_matmul", layer, x, y, ws, stream)
 
 
-def layer_forward(layer: Layer, x: torch.Tensor, y=None, ws=None, stream=None) -> torch.Tensor:
-    return _forward("nq_layer_forward", layer, x, y, ws, stream)
+def layer_forward(layer: Layer, x: torch.Tensor, y=None, ws=None, stream=None, adapters=None, groups=None,
+                  t=None) -> torch.Tensor:
+    """The layer's output; with `adapters` (Adapters of this projection) and `groups` (AdapterRows of
+    this batch), each row's low-rank term added to it (adapter_forward, which fills t if given)."""
+    if adapters is not None and (adapters.d_in != layer.d_in or adapters.d_out != layer.d_out or groups is None):
+        raise ValueError("adapters: of %d x %d with groups %s, the layer is %d x %d" %
+                         (adapters.d_out, adapters.d_in, "given" if groups is not None else "missing", layer.d_out,
+                          layer.d_in))
+    y = _forward("nq_layer_forward", layer, x, y, ws, stream)
+    return y if adapters is None else adapter_forward(adapters, groups, x, y, out=y, t=t, stream=stream)
 
 
 def lrb_transposed(layer: Layer, ybar: torch.Tensor, xbar=None, ws=None, stream=None) -> torch.Tensor:
@@ -420,6 +455,316 @@ def silu_mul(g: torch.Tensor, u: torch.Tensor, h=None, stream=None) -> torch.Ten
     _need(h, "h", torch.bfloat16, shape=tuple(g.shape), device=g.device)
     _check("nq_silu_mul", _lib.nq_silu_mul(_ptr(g), _ptr(u), _ptr(h), g.numel(), _stream_ptr(stream)))
     return h
+
+
+class Adapters:
+    """The low-rank adapters of one projection: A [n][rank][d_in], B [n][d_out][rank] bf16 (rows may
+    be strided), scale [n] fp32 or None (all 1).  Row m with adapter a gets
+    scale[a] * B[a] @ (A[a] @ x[m]) added to the projection's output."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor | None = None):
+        _need(A, "A", torch.bfloat16, contiguous=False)
+        _need(B, "B", torch.bfloat16, device=A.device, contiguous=False)
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+            raise ValueError("A, B: expected [n][rank][d_in] and [n][d_out][rank], got shapes %s and %s" %
+                             (tuple(A.shape), tuple(B.shape)))
+        ld = []
+        for t, name in ((A, "A"), (B, "B")):
+            n, rows, cols = (int(v) for v in t.shape)
+            step = int(t.stride(1)) if rows > 1 else int(t.stride(0)) if n > 1 else cols
+            if 0 in (n, rows, cols) or (cols > 1 and t.stride(2) != 1) or step < cols or (n > 1 and
+                                                                                     t.stride(0) != rows * step):
+                raise ValueError("%s: expected rows of unit stride, evenly spaced over all adapters, got shape %s "
+                                 "strides %s" % (name, tuple(t.shape), tuple(t.stride())))
+            ld.append(step)
+        if scale is not None:
+            _need(scale, "scale", torch.float32, shape=(A.shape[0],), device=A.device)
+        self.A, self.B, self.scale = A, B, scale
+        self.device = A.device
+        self.n, self.rank, self.d_in = (int(v) for v in A.shape)
+        self.d_out = int(B.shape[1])
+        self.struct = nq_adapters(self.n, self.rank, self.d_in, self.d_out, _ptr(A), ld[0], _ptr(B), ld[1],
+                                  _ptr(scale))
+        self._ref = ctypes.byref(self.struct)
+        self._ws = None
+
+    def workspace_bytes(self, M: int) -> int:
+        return int(_lib.nq_adapter_workspace_bytes(self._ref, int(M)))
+
+    def workspace(self, M: int) -> torch.Tensor:
+        """A workspace large enough for M rows, cached here and grown on demand.  Every backward
+        call that passes no ``ws`` uses it: calls that may run at the same time on the GPU, and
+        CUDA graphs that may, must each pass their own."""
+        need = self.workspace_bytes(M)
+        if need == 0:
+            raise NQError("nq_adapter_workspace_bytes", 2)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return self._ws
+
+
+class AdapterRows:
+    """The rows of a batch grouped by adapter: rows [M] int32, offsets [n + 1] int32 (see nq.h)."""
+
+    def __init__(self, rows: torch.Tensor, offsets: torch.Tensor):
+        _need(rows, "rows", torch.int32)
+        _need(offsets, "offsets", torch.int32, device=rows.device)
+        if rows.dim() != 1 or offsets.dim() != 1 or offsets.numel() < 2 or rows.numel() < 1:
+            raise ValueError("rows, offsets: expected [M] and [n + 1], got shapes %s and %s" %
+                             (tuple(rows.shape), tuple(offsets.shape)))
+        self.rows, self.offsets = rows, offsets
+        self.M, self.n = int(rows.numel()), int(offsets.numel()) - 1
+        self._rows_ptr, self._offsets_ptr = _ptr(rows), _ptr(offsets)
+
+
+def adapter_rows(ids: torch.Tensor, n: int, stream=None) -> AdapterRows:
+    """Groups the rows of a batch by adapter: ids [M] int32, values outside 0..n-1 mean none."""
+    _need(ids, "ids", torch.int32)
+    if ids.dim() != 1:
+        raise ValueError("ids: expected [M], got shape %s" % (tuple(ids.shape),))
+    with _on(ids.device):
+        rows = torch.empty_like(ids)
+        offsets = torch.empty(max(int(n), 1) + 1, dtype=torch.int32, device=ids.device)
+        _check("nq_adapter_rows", _lib.nq_adapter_rows(_ptr(ids), ids.numel(), int(n), _ptr(rows), _ptr(offsets),
+                                                       _stream_ptr(stream)))
+    return AdapterRows(rows, offsets)
+
+
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device):
+    """The tensors' device made current for a call (nothing to do where it is already)."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _bf16_rows(t, name: str, M: int, cols: int, device) -> int:
+    """The address of a contiguous [M][cols] bf16 tensor on `device`; _need reports what it is not."""
+    if (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.device == device and
+            t.shape == (M, cols) and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, torch.bfloat16, shape=(M, cols), device=device)
+    return t.data_ptr()
+
+
+def _check_groups(ad: Adapters, groups: AdapterRows, M: int) -> None:
+    if groups.M != M or groups.n != ad.n or groups.rows.device != ad.device:
+        raise ValueError("groups: for %d rows and %d adapters on %s, the call has %d, %d and %s" %
+                         (groups.M, groups.n, groups.rows.device, M, ad.n, ad.device))
+
+
+def adapter_forward(ad: Adapters, groups: AdapterRows, x: torch.Tensor, y: torch.Tensor, out=None, t=None,
+                    stream=None) -> torch.Tensor:
+    """out[m] = y[m] + scale_a B_a A_a x[m] for row m's adapter a (out[m] = y[m] without one).
+    x [M][d_in], y [M][d_out] bf16; out may be y.  t [M][rank] fp32, if given, receives
+    scale_a A_a x[m] for adapter_backward."""
+    dev, M = ad.device, groups.M
+    px = _bf16_rows(x, "x", M, ad.d_in, dev)
+    py = _bf16_rows(y, "y", M, ad.d_out, dev)
+    _check_groups(ad, groups, M)
+    with _on(dev):
+        if out is None:
+            out = torch.empty_like(y)
+        po = _bf16_rows(out, "out", M, ad.d_out, dev)
+        if t is not None:
+            _need(t, "t", torch.float32, shape=(M, ad.rank), device=dev)
+        _check("nq_adapter_forward", _lib.nq_adapter_forward(ad._ref, groups._rows_ptr, groups._offsets_ptr, px, py,
+                                                             po, _ptr(t), M, _stream_ptr(stream)))
+    return out
+
+
+def adapter_backward(ad: Adapters, groups: AdapterRows, x, ybar: torch.Tensor, t, xbar, out=None, gA=None, gB=None,
+                     need_x: bool = True, need_weights: bool = True, ws=None, stream=None):
+    """(xbar + A_a^T u, gA, gB) with u[m] = scale_a B_a^T ybar[m]: the gradients of the input and of
+    the adapters for the output's gradient ybar [M][d_out] bf16.  xbar [M][d_in] bf16 is the shared
+    projection's share (lrb_transposed), out may be xbar; t is what adapter_forward wrote.  gA
+    [n][rank][d_in], gB [n][d_out][rank] bf16, contiguous.  need_x=False leaves xbar out (xbar may
+    be None), need_weights=False leaves gA and gB out (x and t may be None): None in their place."""
+    dev, M = ad.device, groups.M
+    pyb = _bf16_rows(ybar, "ybar", M, ad.d_out, dev)
+    _check_groups(ad, groups, M)
+    px = pt = pxb = po = pa = pb = 0
+    with _on(dev):
+        if need_x:
+            pxb = _bf16_rows(xbar, "xbar", M, ad.d_in, dev)
+            if out is None:
+                out = torch.empty_like(xbar)
+            po = _bf16_rows(out, "out", M, ad.d_in, dev)
+        else:
+            out = None
+        if need_weights:
+            px = _bf16_rows(x, "x", M, ad.d_in, dev)
+            _need(t, "t", torch.float32, shape=(M, ad.rank), device=dev)
+            pt = t.data_ptr()
+            if gA is None:
+                gA = torch.empty((ad.n, ad.rank, ad.d_in), dtype=torch.bfloat16, device=dev)
+            if gB is None:
+                gB = torch.empty((ad.n, ad.d_out, ad.rank), dtype=torch.bfloat16, device=dev)
+            _need(gA, "gA", torch.bfloat16, shape=(ad.n, ad.rank, ad.d_in), device=dev)
+            _need(gB, "gB", torch.bfloat16, shape=(ad.n, ad.d_out, ad.rank), device=dev)
+            pa, pb = gA.data_ptr(), gB.data_ptr()
+        else:
+            gA = gB = None
+        if ws is None:
+            ws = ad.workspace(M)
+        _need_ws(ws, dev)
+        _check("nq_adapter_backward", _lib.nq_adapter_backward(ad._ref, groups._rows_ptr, groups._offsets_ptr, px, pyb,
+                                                               pt, pxb, po, pa, pb, M, ws.data_ptr(), ws.numel(),
+                                                               _stream_ptr(stream)))
+    return out, gA, gB
+
+
+class BlockNorm:
+    """The norms between two blocks (see nq.h): w_pre, w_post [d] bf16 or None (ones); post_norm: the
+    block's output is normed before the residual; alpha: residual scale; w_offset is added to the
+    weights."""
+
+    def __init__(self, d: int, w_pre=None, w_post=None, post_norm: bool = False, alpha: float = 1.0,
+                 eps: float = 1e-5, w_offset: float = 0.0):
+        self.d = int(d)
+        self.device = None
+        for w, name in ((w_pre, "w_pre"), (w_post, "w_post")):
+            if w is not None:
+                _need(w, name, torch.bfloat16, shape=(self.d,), device=self.device)
+                self.device = w.device
+        self.w_pre, self.w_post, self.post_norm = w_pre, w_post, bool(post_norm)
+        self._structs = {}
+        for f32, dtype in ((0, torch.bfloat16), (1, torch.float32)):
+            s = nq_block_norm(self.d, _ptr(w_pre), _ptr(w_post), w_offset, alpha, eps, int(self.post_norm), f32)
+            self._structs[dtype] = (s, ctypes.byref(s))
+        self._ws = {}
+
+    def workspace_bytes(self, M: int) -> int:
+        return int(_lib.nq_block_norm_workspace_bytes(self._structs[torch.float32][1], int(M)))
+
+    def workspace(self, M: int, device=None) -> torch.Tensor:
+        """A workspace large enough for M rows, cached here and grown on demand.  Every backward
+        call that passes no ``ws`` uses it: calls that may run at the same time on the GPU, and
+        CUDA graphs that may, must each pass their own."""
+        device = torch.device(device if device is not None else self.device if self.device is not None else "cuda")
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+        with _on(device):
+            need = self.workspace_bytes(M)
+            if need == 0:
+                raise NQError("nq_block_norm_workspace_bytes", 2)
+            ws = self._ws.get(device)
+            if ws is None or ws.numel() < need:
+                ws = self._ws[device] = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws
+
+    def _struct(self, h):
+        try:
+            return self._structs[h.dtype][1]
+        except KeyError:
+            raise ValueError("h: expected bfloat16 or float32, got %s" % h.dtype) from None
+
+
+def _check_h(norm: BlockNorm, h, name: str):
+    """(M, device) of a residual tensor."""
+    if not isinstance(h, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(h).__name__))
+    if h.dim() != 2 or h.shape[1] != norm.d:
+        raise ValueError("%s: expected [M][%d], got shape %s" % (name, norm.d, tuple(h.shape)))
+    norm._struct(h)
+    _need(h, name, h.dtype, device=norm.device)
+    return int(h.shape[0]), h.device
+
+
+def _check_gate(norm: BlockNorm, gate, M: int, device):
+    """(address, row stride) of a gate [d] (stride 0) or [M][d]."""
+    if gate is None:
+        return 0, 0
+    if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+        _need_rows(gate, "gate", torch.bfloat16, M, norm.d, device=device)
+        if gate.shape[1] != norm.d or gate.stride(0) < norm.d and M > 1:
+            raise ValueError("gate: expected [%d] or [%d][%d], got shape %s strides %s" %
+                             (norm.d, M, norm.d, tuple(gate.shape), tuple(gate.stride())))
+        return gate.data_ptr(), max(int(gate.stride(0)), norm.d)
+    _need(gate, "gate", torch.bfloat16, shape=(norm.d,), device=device)
+    return gate.data_ptr(), 0
+
+
+def block_norm(norm: BlockNorm, y, h: torch.Tensor, gate=None, h_out=None, x=None, stream=None):
+    """(h_out, x): h_out = alpha h + gate * z with z the (normed) block output y, x the normed h_out
+    for the next block.  y [M][d] bf16 or None, h [M][d] bf16 or fp32, gate [d] or [M][d] bf16 or
+    None.  h_out may be h, x may be y."""
+    M, dev = _check_h(norm, h, "h")
+    py = 0 if y is None else _bf16_rows(y, "y", M, norm.d, dev)
+    pg, ldg = _check_gate(norm, gate, M, dev)
+    with _on(dev):
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        elif h_out is not h:
+            _need(h_out, "h_out", h.dtype, shape=(M, norm.d), device=dev)
+        if x is None:
+            x = torch.empty((M, norm.d), dtype=torch.bfloat16, device=dev)
+        px = _bf16_rows(x, "x", M, norm.d, dev)
+        _check("nq_block_norm_forward", _lib.nq_block_norm_forward(norm._struct(h), py, h.data_ptr(), pg, ldg,
+                                                                   h_out.data_ptr(), px, M, _stream_ptr(stream)))
+    return h_out, x
+
+
+def block_norm_backward(norm: BlockNorm, y, h_out: torch.Tensor, gx, gh_out, gate=None, gh=None, gy=None,
+                        g_w_pre=None, g_w_post=None, g_gate=None, need_weights: bool = True, ws=None, stream=None):
+    """(gh, gy, g_w_pre, g_w_post, g_gate) for the gradients gx [M][d] bf16 of x and gh_out (h's type)
+    of h_out; either may be None (zero).  y, gate: as in the forward call, h_out what it returned.
+    gy and g_gate are None without y or gate, g_w_post without post_norm or w_post, g_w_pre without
+    w_pre; need_weights=False leaves g_w_pre, g_w_post and a shared gate's g_gate out.  g_w_pre,
+    g_w_post and the g_gate of one shared gate are fp32 [d], the g_gate of a gate per row bf16
+    [M][d].  gh may be gh_out, gy may be gx."""
+    M, dev = _check_h(norm, h_out, "h_out")
+    d = norm.d
+    py = 0 if y is None else _bf16_rows(y, "y", M, d, dev)
+    pgx = 0 if gx is None else _bf16_rows(gx, "gx", M, d, dev)
+    pg, ldg = _check_gate(norm, gate, M, dev)
+    if gh_out is not None:
+        _need(gh_out, "gh_out", h_out.dtype, shape=(M, d), device=dev)
+
+    def vector(v, name, wanted):
+        if not wanted:
+            return None
+        if v is None:
+            return torch.empty(d, dtype=torch.float32, device=dev)
+        _need(v, name, torch.float32, shape=(d,), device=dev)
+        return v
+
+    with _on(dev):
+        if gh is None:
+            gh = torch.empty_like(h_out)
+        _need(gh, "gh", h_out.dtype, shape=(M, d), device=dev)
+        if y is None:
+            gy = None
+        else:
+            if gy is None:
+                gy = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+            _bf16_rows(gy, "gy", M, d, dev)
+        g_w_pre = vector(g_w_pre, "g_w_pre", need_weights and norm.w_pre is not None)
+        g_w_post = vector(g_w_post, "g_w_post", need_weights and norm.post_norm and norm.w_post is not None and
+                          y is not None)
+        if gate is None or y is None:
+            g_gate = None
+        elif ldg == 0:
+            g_gate = vector(g_gate, "g_gate", need_weights)
+        else:
+            if g_gate is None:
+                g_gate = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+            _bf16_rows(g_gate, "g_gate", M, d, dev)
+        if ws is None:
+            ws = norm.workspace(M, dev)
+        _need_ws(ws, dev)
+        _check("nq_block_norm_backward", _lib.nq_block_norm_backward(
+            norm._struct(h_out), py, h_out.data_ptr(), pg, ldg, pgx, _ptr(gh_out), gh.data_ptr(), _ptr(gy),
+            _ptr(g_w_pre), _ptr(g_w_post), _ptr(g_gate), M, ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+    return gh, gy, g_w_pre, g_w_post, g_gate
 
 
 def selftest_bounded_wait(limit_us: int = 20000, stream=None) -> None:
