@@ -11,6 +11,7 @@
 // blocks' partial t meet in distributed shared memory between the two.  Sums are fp32 in a fixed
 // order; out is rounded once.
 #include "adapter.cuh"
+#include "tc_common.cuh"
 
 namespace nq {
 
@@ -18,26 +19,6 @@ constexpr int kRowsTile = 8;        // rows of a tile
 constexpr int kRowsThreads = 256;
 constexpr int kRowsChunk = 2048;    // K elements of z kept in shared memory at a time
 constexpr int kMaxRank = NQ_ADAPTER_MAX_RANK;
-
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_nctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t local_addr, uint32_t rank) {
-    uint32_t remote;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-    return v;
-}
 
 // V consecutive bf16 (16 bytes at V = 8), as fp32.
 template <int V>
@@ -179,7 +160,7 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
             const int m = e / R, r = e % R;
             const uint32_t addr = static_cast<uint32_t>(__cvta_generic_to_shared(&s.part[m][r]));
             float sum = 0.f;
-            for (uint32_t c = 0; c < nq; ++c) sum += ld_cluster_f32(addr, c);
+            for (uint32_t c = 0; c < nq; ++c) sum += ld_cluster_f32(cluster_map(addr, c));
             s.t[m][r] = sum * scale;
         }
     }

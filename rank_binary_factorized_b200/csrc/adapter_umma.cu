@@ -1,0 +1,511 @@
+// adapter_umma.cu -- low-rank adapters beside a shared projection, on the tensor cores (tcgen05):
+//
+//   t[m] = scale_a P_a z[m],   out[m] = base[m] + Q_a t[m]      (a = the adapter of row m)
+//   forward: z = x, P = A, Q = B;   transposed: z = ybar, P = B^T, Q = A^T
+//
+// Bound: z, base and out cross HBM once each (2 bytes each way against 2 rank flops per element), so
+// the tensor cores are there to keep the products off the critical path and everything else is
+// arranged so that the loads never pause.  One launch does both products:
+//
+// - A tile is up to 128 rows that share an adapter; the rows may lie anywhere (TMA row gathers).  A
+//   cluster of CS blocks takes a tile; block q multiplies K-blocks [KB q / CS, KB (q + 1) / CS) of 64
+//   in the first product and column blocks of 64 in the second, so a few tiles still use most SMs.
+// - Warp 0 loads, warp 1 issues the MMAs, warps 2..5 are the epilogue.  One ring of slots serves both
+//   products (a 128 x 64 tile of z, or of base, and the matching tile of P or Q), so the loads of
+//   the second product, and of the cluster's next tile, are in flight while t is put together.
+// - The blocks' partial t go to the block that owns the row (128 / CS rows each) through distributed
+//   shared memory; it adds them in rank order, scales, writes t and sends the row to every block as
+//   the sum of two bf16 values (16 bits of t: rounding t itself to bf16 would add half a unit of its
+//   own to the result), in the layout that the second product's A operand has.
+// - The epilogue adds the accumulator to the tile of base in shared memory and stores whole row pieces.
+#include <algorithm>
+#include <atomic>
+
+#include "adapter.cuh"
+#include "tc_common.cuh"
+
+namespace nq {
+
+constexpr int kTok = 128;                  // rows of a tile: the MMA's M
+constexpr int kStep = 64;                  // K or N elements of a slot
+constexpr uint32_t kTokBytes = kTok * 128; // 128 rows x 64 bf16
+constexpr int kUmmaThreads = 192;
+constexpr int kMaxSlots = 8;
+constexpr uint32_t kAccCol = 128;          // the second product's accumulators, 64 columns each
+constexpr uint32_t kTmemColumns = 256;
+
+struct AdapterUmmaArgs {
+    AdapterArgs a;
+    int slots;
+    uint32_t slot_bytes;
+    int panels;   // 64-element panels of the rank
+    int r16;      // rank rounded up to the MMA's K
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
+}
+
+// What v's bf16 part leaves of it (nothing of an infinity).
+__device__ __forceinline__ float rest_of(float v, uint32_t part) {
+    const float p = __uint_as_float(part);
+    return isinf(p) ? 0.f : v - p;
+}
+
+template <bool BWD>
+__global__ void __launch_bounds__(kUmmaThreads, 1)
+    adapter_umma_kernel(const __grid_constant__ CUtensorMap map_z, const __grid_constant__ CUtensorMap map_base,
+                        const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const AdapterUmmaArgs ua) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const AdapterArgs& a = ua.a;
+    const uint32_t smem_base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int slots = ua.slots, panels = ua.panels, r16 = ua.r16;
+    const uint32_t cs = cluster_nctarank(), q = cluster_ctarank();
+    const int own_rows = kTok / static_cast<int>(cs);  // rows of t that a block puts together
+    const uint32_t part_bytes = static_cast<uint32_t>(panels) * kTokBytes;
+    const uint32_t t_base = smem_base + slots * ua.slot_bytes;  // [2 parts][panels][128 rows][128 B], swizzled
+    const uint32_t inbox = t_base + 2 * part_bytes;             // [cs][own_rows][r16] fp32
+    const uint32_t bars = inbox + kTok * r16 * 4;
+    auto slot_at = [&](int s) { return smem_base + s * ua.slot_bytes; };
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto free1 = [&](int s) { return bars + 8u * (kMaxSlots + s); };      // first product: its MMAs are done
+    auto free2 = [&](int s) { return bars + 8u * (2 * kMaxSlots + s); };  // second: the epilogue is done
+    const uint32_t acc1_full = bars + 8u * (3 * kMaxSlots), acc1_empty = acc1_full + 8u;
+    auto acc2_full = [&](int i) { return acc1_full + 16u + 8u * i; };
+    auto acc2_empty = [&](int i) { return acc1_full + 32u + 8u * i; };
+    const uint32_t inbox_full = acc1_full + 48u, t_full = acc1_full + 56u, drain = acc1_full + 64u;
+    const uint32_t tmem_slot = acc1_full + 72u;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned int* err = a.err;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < slots; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(free1(s), 1);
+            tc::mbar_init(free2(s), 4);
+        }
+        tc::mbar_init(acc1_full, 1);
+        tc::mbar_init(acc1_empty, 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(acc2_full(i), 1);
+            tc::mbar_init(acc2_empty(i), 4);
+        }
+        // every block sends the rows that this one owns, from the warps that hold them
+        tc::mbar_init(inbox_full, cs * static_cast<uint32_t>(max(1, own_rows / 32)));
+        tc::mbar_init(t_full, cs * 4u);
+        tc::mbar_init(drain, 1);
+        tc::mbar_fence_init();
+        tc::tma_prefetch_desc(&map_z);
+        tc::tma_prefetch_desc(&map_base);
+        tc::tma_prefetch_desc(&map_a);
+        tc::tma_prefetch_desc(&map_b);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, kTmemColumns);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    cluster_arrive();  // the barriers of every block are set up before another one arrives on them
+    cluster_wait();
+    tc::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
+
+    const int kb_all = static_cast<int>((a.K + kStep - 1) / kStep), nb_all = static_cast<int>((a.N + kStep - 1) / kStep);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * q / cs);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (q + 1) / cs);
+    const int nb0 = a.out ? static_cast<int>(static_cast<int64_t>(nb_all) * q / cs) : 0;
+    const int nb1 = a.out ? static_cast<int>(static_cast<int64_t>(nb_all) * (q + 1) / cs) : 0;
+    const uint32_t w1_bytes = BWD ? panels * 8192u : r16 * 128u;
+    const uint32_t w2_bytes = BWD ? r16 * 128u : panels * 8192u;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loads
+        uint32_t it = 0, was2 = 0, ph1 = 0, ph2 = 0;  // bit s: slot s's last use and barrier phases
+        int s = 0;
+        bool ok = true;
+        auto next = [&](bool second) {  // waits until slot s may be written
+            if (it >= static_cast<uint32_t>(slots)) {
+                const uint32_t bit = 1u << s;
+                if (lane == 0) ok = (was2 & bit) ? tc::mbar_wait(free2(s), (ph2 >> s) & 1u, err)
+                                                 : tc::mbar_wait(free1(s), (ph1 >> s) & 1u, err);
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (was2 & bit) ph2 ^= bit; else ph1 ^= bit;
+            }
+            was2 = second ? was2 | (1u << s) : was2 & ~(1u << s);
+            return ok;
+        };
+        for (int tile = blockIdx.x; ok; tile += gridDim.x) {
+            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
+            if (t.adapter < 0) break;
+            if (t.adapter >= a.n) continue;
+            const int quads = (t.count + 3) / 4;
+            int32_t row[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = lane * 4 + i;
+                const int r = e < t.count ? checked_row(a.rows, t.first + e, a.M, err) : -1;
+                row[i] = r >= 0 ? r : static_cast<int32_t>(a.M);  // past the last row: zeros
+            }
+            auto load = [&](bool second, int b) {
+                if (!next(second)) return false;
+                const uint32_t tok = slot_at(s), w = tok + kTokBytes, bar = full(s);
+                if (lane == 0) tc::mbar_arrive_expect_tx(bar, quads * 512u + (second ? w2_bytes : w1_bytes));
+                __syncwarp();
+                if (lane < quads) tc::tma_gather4(tok + lane * 512u, second ? &map_base : &map_z, b * kStep, row, bar);
+                if (lane == 0) {
+                    if (second == BWD) {  // A: [rank][64 of d_in]
+                        tc::tma_load_3d(w, &map_a, b * kStep, 0, t.adapter, bar);
+                    } else {  // B: [64 of d_out][rank], in panels of 64 ranks
+                        for (int p = 0; p < panels; ++p)
+                            tc::tma_load_3d(w + p * 8192u, &map_b, p * 64, b * kStep, t.adapter, bar);
+                    }
+                }
+                ++it;
+                if (++s == slots) s = 0;
+                return true;
+            };
+            for (int b = kb0; b < kb1 && ok; ++b) ok = load(false, b);
+            for (int b = nb0; b < nb1 && ok; ++b) ok = load(true, b);
+        }
+        // every load issued has landed before the block may end
+        if (lane == 0) {
+            const uint32_t first = it > static_cast<uint32_t>(slots) ? it - slots : 0u;
+            for (uint32_t j = first; j < it; ++j) tc::mbar_wait(full(j % slots), (j / slots) & 1u, err);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMAs
+        const uint32_t idesc1 = tc::idesc_bf16_f32(kTok, r16, false, BWD);
+        const uint32_t idesc2 = tc::idesc_bf16_f32(kTok, kStep, false, BWD);
+        uint32_t it = 0, tiles = 0, acc2 = 0;
+        int s = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok; tile += gridDim.x) {
+            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
+            if (t.adapter < 0) break;
+            if (t.adapter >= a.n) continue;
+            if (lane == 0) {
+                if (kb1 > kb0) {
+                    ok = tc::mbar_wait(acc1_empty, (tiles & 1u) ^ 1u, err);
+                    tc::tc_fence_after();
+                    for (int b = kb0; b < kb1 && ok; ++b) {
+                        if (!(ok = tc::mbar_wait(full(s), (it / slots) & 1u, err))) break;
+                        tc::tc_fence_after();
+                        const uint32_t tok = slot_at(s), w = tok + kTokBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kStep / 16; ++kk) {
+                            const uint64_t ad = tc::smem_desc_sw128(tok + kk * 32u, 16u, 1024u);
+                            const uint64_t bd = BWD ? tc::smem_desc_sw128(w + kk * 2048u, 8192u, 1024u)
+                                                    : tc::smem_desc_sw128(w + kk * 32u, 16u, 1024u);
+                            tc::mma_f16_ss(tmem, ad, bd, idesc1, (b > kb0 || kk > 0) ? 1u : 0u);
+                        }
+                        tc::mma_commit(free1(s));
+                        ++it;
+                        if (++s == slots) s = 0;
+                    }
+                    if (ok) tc::mma_commit(acc1_full);
+                }
+                if (ok && nb1 > nb0) {
+                    ok = tc::mbar_wait_cluster(t_full, tiles & 1u, err);
+                    tc::fence_proxy_async_smem();  // t was written by threads
+                    tc::tc_fence_after();
+                    for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
+                        const int i = acc2 & 1;
+                        if (!(ok = tc::mbar_wait(acc2_empty(i), ((acc2 >> 1) & 1u) ^ 1u, err))) break;
+                        if (!(ok = tc::mbar_wait(full(s), (it / slots) & 1u, err))) break;
+                        tc::tc_fence_after();
+                        const uint32_t w = slot_at(s) + kTokBytes, d = tmem + kAccCol + i * kStep;
+                        for (int part = 0; part < 2; ++part) {
+                            for (int kk = 0; kk < r16 / 16; ++kk) {
+                                const uint32_t p = kk / 4, in = kk % 4;
+                                const uint64_t ad = tc::smem_desc_sw128(
+                                    t_base + part * part_bytes + p * kTokBytes + in * 32u, 16u, 1024u);
+                                const uint64_t bd = BWD ? tc::smem_desc_sw128(w + kk * 2048u, 8192u, 1024u)
+                                                        : tc::smem_desc_sw128(w + p * 8192u + in * 32u, 16u, 1024u);
+                                tc::mma_f16_ss(d, ad, bd, idesc2, (part > 0 || kk > 0) ? 1u : 0u);
+                            }
+                        }
+                        tc::mma_commit(acc2_full(i));
+                        ++it;
+                        if (++s == slots) s = 0;
+                    }
+                }
+            }
+            ++tiles;
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
+        if (lane == 0) {  // every MMA issued has completed before TMEM is released
+            tc::mma_commit(drain);
+            tc::mbar_wait(drain, 0u, err);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        const int w4 = warp & 3;  // TMEM lanes 32 w4 .. 32 w4 + 31
+        const int tid = w4 * 32 + lane;
+        uint32_t it = 0, tiles = 0, acc2 = 0;
+        int s = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok; tile += gridDim.x) {
+            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
+            if (t.adapter < 0) break;
+            const int my_row = tid < t.count ? checked_row(a.rows, t.first + tid, a.M, err) : -1;
+            if (t.adapter >= a.n) {
+                // rows without an adapter: t = 0, out = base (this block's columns)
+                if (a.t && q == 0 && my_row >= 0)
+                    for (int r = 0; r < a.rank; ++r) a.t[static_cast<int64_t>(my_row) * a.rank + r] = 0.f;
+                if (a.out && a.out != a.base) {
+                    const int64_t c0 = static_cast<int64_t>(nb0) * kStep;
+                    const int64_t c1 = min(a.N, static_cast<int64_t>(nb1) * kStep);
+                    for (int m = 0; m < 32; ++m) {
+                        const int row = __shfl_sync(0xFFFFFFFFu, my_row, m);
+                        if (row < 0) continue;
+                        const uint16_t* src = a.base + static_cast<int64_t>(row) * a.N;
+                        uint16_t* dst = a.out + static_cast<int64_t>(row) * a.N;
+#pragma unroll 4
+                        for (int64_t c = c0 + lane * 8; c < c1; c += 256)
+                            *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
+                    }
+                }
+                continue;
+            }
+            // ---- this block's share of t, to the rows' owners
+            if (tiles > 0) ok = tc::mbar_wait_cluster(t_full, (tiles & 1u) ^ 1u, err);  // their inboxes are read
+            if (ok && kb1 > kb0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t owner = static_cast<uint32_t>(tid / own_rows);
+            const uint32_t to = cluster_map(inbox + (q * own_rows + tid % own_rows) * r16 * 4u, owner);
+            for (int c0 = 0; c0 < r16; c0 += 32) {
+                uint32_t v[32];
+                if (kb1 > kb0) {
+                    tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + c0, v);
+                    tc::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    if (c0 + j < r16) st_cluster_v4(to + (c0 + j) * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
+            }
+            tc::tc_fence_before();
+            fence_cluster();
+            __syncwarp();
+            if (lane == 0 && kb1 > kb0) tc::mbar_arrive(acc1_empty);
+            if (own_rows >= 32) {
+                if (lane == 0) tc::mbar_arrive_cluster(cluster_map(inbox_full, owner));
+            } else if (lane % own_rows == 0) {
+                tc::mbar_arrive_cluster(cluster_map(inbox_full, owner));
+            }
+            // ---- the rows this block owns
+            ok = tc::mbar_wait_cluster(inbox_full, tiles & 1u, err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const float scale = a.scale ? a.scale[t.adapter] : 1.f;
+            const int per_row = r16 / 8;
+            for (int e = tid; e < own_rows * per_row; e += 128) {
+                const int rr = e / per_row, c = e % per_row, m = static_cast<int>(q) * own_rows + rr;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                if (m < t.count) {
+                    for (uint32_t src = 0; src < cs; ++src) {
+                        const uint32_t at = inbox + ((src * own_rows + rr) * r16 + c * 8) * 4u;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float f[4];
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                                         : "r"(at + 16u * j)
+                                         : "memory");
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[4 * j + i] += f[i];
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = c * 8 + j < a.rank ? v[j] * scale : 0.f;
+                    if (a.t) {
+                        const int row = a.rows[t.first + m];
+                        if (row >= 0 && row < a.M) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (c * 8 + j < a.rank) a.t[static_cast<int64_t>(row) * a.rank + c * 8 + j] = v[j];
+                        }
+                    }
+                }
+                if (!a.out) continue;
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    hi[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                    lo[j] = pack_bf16(rest_of(v[2 * j], hi[j] << 16), rest_of(v[2 * j + 1], hi[j] & 0xFFFF0000u));
+                }
+                const uint32_t at = t_base + (c / 8) * kTokBytes + m * 128u + (((c % 8) ^ (m & 7)) << 4);
+                for (uint32_t dst = 0; dst < cs; ++dst) {
+                    const uint32_t remote = cluster_map(at, dst);
+                    st_cluster_v4(remote, hi[0], hi[1], hi[2], hi[3]);
+                    st_cluster_v4(remote + part_bytes, lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");  // the tensor cores read t
+            fence_cluster();
+            __syncwarp();
+            if (lane < static_cast<int>(cs)) tc::mbar_arrive_cluster(cluster_map(t_full, lane));
+            // ---- out = base + the second product
+            it += kb1 - kb0;
+            s = it % slots;
+            for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
+                const int i = acc2 & 1;
+                ok = tc::mbar_wait(full(s), (it / slots) & 1u, err) && tc::mbar_wait(acc2_full(i), (acc2 >> 1) & 1u, err);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint32_t line = slot_at(s) + tid * 128u;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t v[32];
+                    tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kAccCol + i * kStep + half * 32,
+                                           v);
+                    tc::tmem_wait_ld();
+                    if (my_row >= 0) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t at = line + (((half * 4 + c) ^ (lane & 7)) << 4);
+                            uint32_t y[4];
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                                         : "r"(at)
+                                         : "memory");
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                y[j] = pack_bf16(__uint_as_float(y[j] << 16) + __uint_as_float(v[c * 8 + 2 * j]),
+                                                 __uint_as_float(y[j] & 0xFFFF0000u) +
+                                                     __uint_as_float(v[c * 8 + 2 * j + 1]));
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]),
+                                         "r"(y[2]), "r"(y[3])
+                                         : "memory");
+                        }
+                    }
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(acc2_empty(i));
+                // eight lanes store the 128 bytes of a row
+                const int64_t col = static_cast<int64_t>(b) * kStep + (lane & 7) * 8;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const int m = g * 4 + (lane >> 3);
+                    const int row = __shfl_sync(0xFFFFFFFFu, my_row, m);
+                    if (row >= 0 && col < a.N) {
+                        uint4 y;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                     : "r"(slot_at(s) + (w4 * 32 + m) * 128u + (((lane & 7) ^ (m & 7)) << 4))
+                                     : "memory");
+                        *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row) * a.N + col) = y;
+                    }
+                }
+                tc::fence_proxy_async_smem();  // the slot is written by a TMA load next
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(free2(s));
+                ++it;
+                if (++s == slots) s = 0;
+            }
+            ++tiles;
+        }
+    }
+
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, kTmemColumns);
+    }
+    cluster_arrive();  // no block of the cluster writes to this one's shared memory any more
+    cluster_wait();
+}
+
+}  // namespace nq
+
+// ------------------------------------------------------------------------------ host side
+namespace {
+
+constexpr size_t kUmmaSmemMax = 227 * 1024;
+
+// bf16 tensor of `dims` dimensions, innermost first, 128-byte swizzle.
+bool tmap_bf16(CUtensorMap* map, const void* base, int dims, const int64_t* extent, const int64_t* stride_elems,
+               const int* box) {
+    auto enc = nq_host::tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t d[3], st[2];
+    cuuint32_t bx[3], es[3] = {1, 1, 1};
+    for (int i = 0; i < dims; ++i) {
+        d[i] = static_cast<cuuint64_t>(extent[i]);
+        bx[i] = static_cast<cuuint32_t>(box[i]);
+        if (i > 0) st[i - 1] = static_cast<cuuint64_t>(stride_elems[i - 1]) * 2;
+    }
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(dims), const_cast<void*>(base), d, st, bx, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Every row of z, base, A and B starts on 16 bytes, as TMA needs.
+bool nq_adapter_umma_fits(const nq::AdapterArgs& a) {
+    return a.K % 8 == 0 && a.N % 8 == 0 && a.lda % 8 == 0 && a.ldb % 8 == 0;
+}
+
+nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl) {
+    nq::AdapterUmmaArgs ua{};
+    ua.a = a;
+    ua.r16 = (a.rank + 15) / 16 * 16;
+    ua.panels = (a.rank + 63) / 64;
+    ua.slot_bytes = nq::kTokBytes + static_cast<uint32_t>(ua.panels) * 8192u;
+    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + nq::kTok * ua.r16 * 4 +
+                         8 * (3 * nq::kMaxSlots) + 80;
+    ua.slots = static_cast<int>(std::min<size_t>(nq::kMaxSlots, (kUmmaSmemMax - fixed) / ua.slot_bytes));
+    const size_t smem = fixed + ua.slots * static_cast<size_t>(ua.slot_bytes);
+
+    CUtensorMap mz, mbase, ma, mb;
+    const int gather_box[2] = {64, 1}, a_box[3] = {64, ua.r16, 1}, b_box[3] = {64, 64, 1};
+    const int64_t z_dims[2] = {a.K, a.M}, base_dims[2] = {a.N, a.M};
+    const int64_t a_dims[3] = {a.d_in, a.rank, a.n}, a_st[2] = {a.lda, a.lda * a.rank};
+    const int64_t b_dims[3] = {a.rank, a.d_out, a.n}, b_st[2] = {a.ldb, a.ldb * a.d_out};
+    if (!tmap_bf16(&mz, a.z, 2, z_dims, &a.K, gather_box) ||
+        !tmap_bf16(&mbase, a.out ? a.base : a.z, 2, a.out ? base_dims : z_dims, a.out ? &a.N : &a.K, gather_box) ||
+        !tmap_bf16(&ma, a.A, 3, a_dims, a_st, a_box) || !tmap_bf16(&mb, a.B, 3, b_dims, b_st, b_box))
+        return NQ_ERR_LAUNCH;
+
+    const void* fn = backward ? reinterpret_cast<const void*>(nq::adapter_umma_kernel<true>)
+                              : reinterpret_cast<const void*>(nq::adapter_umma_kernel<false>);
+    static std::atomic<bool> attr_done[64];  // per device; setting an attribute twice is harmless
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return NQ_ERR_DEVICE;
+    if (!attr_done[dev].load(std::memory_order_acquire)) {
+        for (const void* f : {reinterpret_cast<const void*>(nq::adapter_umma_kernel<true>),
+                              reinterpret_cast<const void*>(nq::adapter_umma_kernel<false>)})
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kUmmaSmemMax)) !=
+                cudaSuccess)
+                return NQ_ERR_LAUNCH;
+        attr_done[dev].store(true, std::memory_order_release);
+    }
+    // The fewest tiles that M rows can make decide how many blocks share one (at most a portable
+    // cluster); clusters loop over the tiles that a finer grouping adds.
+    const int64_t sms = nq_host::sm_count(), least = (a.M + nq::kTok - 1) / nq::kTok;
+    int cs = 8;
+    while (cs > 1 && least * cs > sms) cs /= 2;
+    const int64_t clusters = std::min(nq::max_adapter_tiles(a.M, a.n, nq::kTok), std::max<int64_t>(1, sms / cs));
+    void* kargs[] = {&mz, &mbase, &ma, &mb, &ua};
+    return nq_host::launch_ex(fn, dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(cs)),
+                              dim3(nq::kUmmaThreads), smem, stream, kargs, pdl, cs) == cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_LAUNCH;
+}

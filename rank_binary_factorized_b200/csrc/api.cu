@@ -31,6 +31,8 @@ nq_status nq_launch_sign_grads(const nq_lrb_layer* L, const nq_lrb_layer* X, con
                                int64_t M, float* gU, int64_t ldgu, float* gV, int64_t ldgv, void* ws,
                                cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_rows(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl);
+bool nq_adapter_umma_fits(const nq::AdapterArgs& a);
+nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_grad_any(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_group_rows(const int32_t* ids, int64_t M, int n, int32_t* rows, int32_t* offsets,
                                        cudaStream_t stream, bool pdl);
@@ -470,6 +472,11 @@ nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const in
     return a;
 }
 
+nq_status launch_adapter(const nq::AdapterArgs& a, bool backward, cudaStream_t stream) {
+    if (a.M > 16 && nq_adapter_umma_fits(a)) return nq_launch_adapter_umma(a, backward, stream, pdl_enabled());
+    return nq_launch_adapter_rows(a, backward, stream, pdl_enabled());
+}
+
 }  // namespace
 
 nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32_t* rows, int32_t* offsets, void* stream) {
@@ -503,7 +510,7 @@ nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, const in
     a.t = t;
     a.K = S->d_in;
     a.N = S->d_out;
-    return nq_launch_adapter_rows(a, false, static_cast<cudaStream_t>(stream), pdl_enabled());
+    return launch_adapter(a, false, static_cast<cudaStream_t>(stream));
 }
 
 nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets, const uint16_t* x,
@@ -528,7 +535,7 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
         a.t = gA ? u : nullptr;
         a.K = S->d_out;
         a.N = S->d_in;
-        if ((st = nq_launch_adapter_rows(a, true, s, pdl_enabled())) != NQ_OK) return st;
+        if ((st = launch_adapter(a, true, s)) != NQ_OK) return st;
     }
     if (!gA && !gB) return NQ_OK;
     nq::AdapterGradArgs g{};
