@@ -46,6 +46,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
 }
 
+// Two bf16 values and two fp32 addends, rounded once.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t y, uint32_t lo, uint32_t hi) {
+    return pack_bf16(__uint_as_float(y << 16) + __uint_as_float(lo),
+                     __uint_as_float(y & 0xFFFF0000u) + __uint_as_float(hi));
+}
+
 // What v's bf16 part leaves of it (nothing of an infinity).
 __device__ __forceinline__ float rest_of(float v, uint32_t part) {
     const float p = __uint_as_float(part);
@@ -54,9 +60,10 @@ __device__ __forceinline__ float rest_of(float v, uint32_t part) {
 
 template <bool BWD>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
-    adapter_umma_kernel(const __grid_constant__ CUtensorMap map_z, const __grid_constant__ CUtensorMap map_base,
-                        const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                        const AdapterUmmaArgs ua) {
+    adapter_umma_kernel(const __grid_constant__ CUtensorMap map_z, const __grid_constant__ CUtensorMap map_z1,
+                        const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base1,
+                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ CUtensorMap map_b, const AdapterUmmaArgs ua) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const AdapterArgs& a = ua.a;
     const uint32_t smem_base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -66,7 +73,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t part_bytes = static_cast<uint32_t>(panels) * kTokBytes;
     const uint32_t t_base = smem_base + slots * ua.slot_bytes;  // [2 parts][panels][128 rows][128 B], swizzled
     const uint32_t inbox = t_base + 2 * part_bytes;             // [cs][own_rows][r16] fp32
-    const uint32_t bars = inbox + kTok * r16 * 4;
+    // neighbouring rows of the inbox use different banks: their 16-byte pieces are permuted where a
+    // row fills whole 128-byte lines, else the rows are padded
+    const uint32_t inbox_mix = r16 % 32 == 0 ? 7u : 0u, inbox_ld = r16 * 4u + (inbox_mix ? 0u : 16u);
+    const uint32_t bars = inbox + kTok * inbox_ld;
     auto slot_at = [&](int s) { return smem_base + s * ua.slot_bytes; };
     auto full = [&](int s) { return bars + 8u * s; };
     auto free1 = [&](int s) { return bars + 8u * (kMaxSlots + s); };      // first product: its MMAs are done
@@ -97,9 +107,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         tc::mbar_init(drain, 1);
         tc::mbar_fence_init();
         tc::tma_prefetch_desc(&map_z);
-        tc::tma_prefetch_desc(&map_base);
         tc::tma_prefetch_desc(&map_a);
         tc::tma_prefetch_desc(&map_b);
+        tc::tma_prefetch_desc(&map_base);
+        tc::tma_prefetch_desc(&map_out);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, kTmemColumns);
@@ -107,8 +118,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     }
     tc::tc_fence_before();
     __syncthreads();
-    cluster_arrive();  // the barriers of every block are set up before another one arrives on them
-    cluster_wait();
+    // Waited for before another block's barriers are used, by each warp where it can afford to: with
+    // one block and no cluster launch, a wait by some of the warps did not return before the others'.
+    if (cs > 1) cluster_arrive();
     tc::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
 
@@ -142,27 +154,56 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
             if (t.adapter < 0) break;
             if (t.adapter >= a.n) continue;
-            const int quads = (t.count + 3) / 4;
+            // lane l holds entries 4 l .. 4 l + 3; eight lanes hold a group of 32 rows, which one TMA
+            // box fetches where the rows follow one another (it may fetch rows past the tile's last:
+            // they reach no output), and row gathers where they do not
             int32_t row[4];
+            bool follow = true;
+            const int first32 = __shfl_sync(0xFFFFFFFFu, 4 * lane < t.count ? a.rows[t.first + 4 * lane] : -1, lane & 24);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int e = lane * 4 + i;
                 const int r = e < t.count ? checked_row(a.rows, t.first + e, a.M, err) : -1;
+                follow = follow && (e >= t.count || (r >= 0 && r == first32 + (e & 31)));
                 row[i] = r >= 0 ? r : static_cast<int32_t>(a.M);  // past the last row: zeros
+            }
+            const bool used = 4 * lane < t.count;
+            const bool box = ((__ballot_sync(0xFFFFFFFFu, follow) >> (lane & 24)) & 0xFFu) == 0xFFu;
+            const bool loads = used && (!box || (lane & 7) == 0);
+            uint32_t z_bytes = loads ? (box ? 4096u : 512u) : 0u;  // of all the lanes' loads
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) z_bytes += __shfl_xor_sync(0xFFFFFFFFu, z_bytes, o);
+            bool boxes = true;  // every group that has rows is a box
+            int32_t row0[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                row0[g] = __shfl_sync(0xFFFFFFFFu, row[0], 8 * g);
+                boxes = boxes && (__shfl_sync(0xFFFFFFFFu, box || !used, 8 * g) != 0);
             }
             auto load = [&](bool second, int b) {
                 if (!next(second)) return false;
                 const uint32_t tok = slot_at(s), w = tok + kTokBytes, bar = full(s);
-                if (lane == 0) tc::mbar_arrive_expect_tx(bar, quads * 512u + (second ? w2_bytes : w1_bytes));
-                __syncwarp();
-                if (lane < quads) tc::tma_gather4(tok + lane * 512u, second ? &map_base : &map_z, b * kStep, row, bar);
-                if (lane == 0) {
+                if (tc::elect_one()) {
+                    tc::mbar_arrive_expect_tx(bar, z_bytes + (second ? w2_bytes : w1_bytes));
                     if (second == BWD) {  // A: [rank][64 of d_in]
                         tc::tma_load_3d(w, &map_a, b * kStep, 0, t.adapter, bar);
                     } else {  // B: [64 of d_out][rank], in panels of 64 ranks
                         for (int p = 0; p < panels; ++p)
                             tc::tma_load_3d(w + p * 8192u, &map_b, p * 64, b * kStep, t.adapter, bar);
                     }
+                    if (boxes) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (32 * g < t.count)
+                                tc::tma_load_2d(tok + g * 4096u, second ? &map_base : &map_z, b * kStep, row0[g], bar);
+                    }
+                }
+                __syncwarp();
+                if (!boxes && loads) {
+                    if (box)
+                        tc::tma_load_2d(tok + lane * 512u, second ? &map_base : &map_z, b * kStep, row[0], bar);
+                    else
+                        tc::tma_gather4(tok + lane * 512u, second ? &map_base1 : &map_z1, b * kStep, row, bar);
                 }
                 ++it;
                 if (++s == slots) s = 0;
@@ -177,6 +218,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             for (uint32_t j = first; j < it; ++j) tc::mbar_wait(full(j % slots), (j / slots) & 1u, err);
         }
         __syncwarp();
+        if (cs > 1) cluster_wait();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMAs
         const uint32_t idesc1 = tc::idesc_bf16_f32(kTok, r16, false, BWD);
@@ -184,17 +226,19 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         uint32_t it = 0, tiles = 0, acc2 = 0;
         int s = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok; tile += gridDim.x) {
-            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
-            if (t.adapter < 0) break;
+        int tile = blockIdx.x;
+        AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err), t_next;
+        for (; ok && t.adapter >= 0; t = t_next) {
+            tile += gridDim.x;
+            t_next = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
             if (t.adapter >= a.n) continue;
-            if (lane == 0) {
-                if (kb1 > kb0) {
-                    ok = tc::mbar_wait(acc1_empty, (tiles & 1u) ^ 1u, err);
+            if (kb1 > kb0) {
+                ok = tc::mbar_wait(acc1_empty, (tiles & 1u) ^ 1u, err);
+                for (int b = kb0; b < kb1 && ok; ++b) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(full(s), (it / slots) & 1u, err));
+                    if (!ok) break;
                     tc::tc_fence_after();
-                    for (int b = kb0; b < kb1 && ok; ++b) {
-                        if (!(ok = tc::mbar_wait(full(s), (it / slots) & 1u, err))) break;
-                        tc::tc_fence_after();
+                    if (tc::elect_one()) {
                         const uint32_t tok = slot_at(s), w = tok + kTokBytes;
 #pragma unroll
                         for (int kk = 0; kk < kStep / 16; ++kk) {
@@ -204,45 +248,54 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                             tc::mma_f16_ss(tmem, ad, bd, idesc1, (b > kb0 || kk > 0) ? 1u : 0u);
                         }
                         tc::mma_commit(free1(s));
-                        ++it;
-                        if (++s == slots) s = 0;
+                        if (b + 1 == kb1) tc::mma_commit(acc1_full);
                     }
-                    if (ok) tc::mma_commit(acc1_full);
+                    __syncwarp();
+                    ++it;
+                    if (++s == slots) s = 0;
                 }
-                if (ok && nb1 > nb0) {
-                    ok = tc::mbar_wait_cluster(t_full, tiles & 1u, err);
-                    tc::fence_proxy_async_smem();  // t was written by threads
+            }
+            if (ok && nb1 > nb0) {
+                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_cluster(t_full, tiles & 1u, err));
+                tc::fence_proxy_async_smem();  // t was written by threads
+                tc::tc_fence_after();
+                for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
+                    const int i = acc2 & 1;
+                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc2_empty(i), ((acc2 >> 1) & 1u) ^ 1u, err) &&
+                                                     tc::mbar_wait(full(s), (it / slots) & 1u, err));
+                    if (!ok) break;
                     tc::tc_fence_after();
-                    for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
-                        const int i = acc2 & 1;
-                        if (!(ok = tc::mbar_wait(acc2_empty(i), ((acc2 >> 1) & 1u) ^ 1u, err))) break;
-                        if (!(ok = tc::mbar_wait(full(s), (it / slots) & 1u, err))) break;
-                        tc::tc_fence_after();
+                    if (tc::elect_one()) {
                         const uint32_t w = slot_at(s) + kTokBytes, d = tmem + kAccCol + i * kStep;
-                        for (int part = 0; part < 2; ++part) {
-                            for (int kk = 0; kk < r16 / 16; ++kk) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            if (kk * 16 < r16) {
                                 const uint32_t p = kk / 4, in = kk % 4;
-                                const uint64_t ad = tc::smem_desc_sw128(
-                                    t_base + part * part_bytes + p * kTokBytes + in * 32u, 16u, 1024u);
                                 const uint64_t bd = BWD ? tc::smem_desc_sw128(w + kk * 2048u, 8192u, 1024u)
                                                         : tc::smem_desc_sw128(w + p * 8192u + in * 32u, 16u, 1024u);
-                                tc::mma_f16_ss(d, ad, bd, idesc2, (part > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                                for (int part = 0; part < 2; ++part) {
+                                    const uint64_t ad = tc::smem_desc_sw128(
+                                        t_base + part * part_bytes + p * kTokBytes + in * 32u, 16u, 1024u);
+                                    tc::mma_f16_ss(d, ad, bd, idesc2, (part > 0 || kk > 0) ? 1u : 0u);
+                                }
                             }
                         }
                         tc::mma_commit(acc2_full(i));
-                        ++it;
-                        if (++s == slots) s = 0;
                     }
+                    __syncwarp();
+                    ++it;
+                    if (++s == slots) s = 0;
                 }
             }
             ++tiles;
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        }
-        if (lane == 0) {  // every MMA issued has completed before TMEM is released
-            tc::mma_commit(drain);
-            tc::mbar_wait(drain, 0u, err);
         }
         __syncwarp();
+        if (tc::elect_one()) tc::mma_commit(drain);  // every MMA issued has completed before TMEM is released
+        __syncwarp();
+        tc::mbar_wait(drain, 0u, err);
+        __syncwarp();
+        if (cs > 1) cluster_wait();
     } else {
         // ---------------------------------------------------------------- epilogue
         const int w4 = warp & 3;  // TMEM lanes 32 w4 .. 32 w4 + 31
@@ -250,9 +303,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         uint32_t it = 0, tiles = 0, acc2 = 0;
         int s = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok; tile += gridDim.x) {
-            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
-            if (t.adapter < 0) break;
+        int tile = blockIdx.x;
+        AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err), t_next;
+        if (cs > 1) cluster_wait();  // every block's barriers are set up
+        for (; ok && t.adapter >= 0; t = t_next) {
+            tile += gridDim.x;
+            t_next = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
             const int my_row = tid < t.count ? checked_row(a.rows, t.first + tid, a.M, err) : -1;
             if (t.adapter >= a.n) {
                 // rows without an adapter: t = 0, out = base (this block's columns)
@@ -273,6 +329,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 }
                 continue;
             }
+            // the 32 rows of this warp: all there and in a row, so that one TMA store takes a box
+            const int row0 = __shfl_sync(0xFFFFFFFFu, my_row, 0);
+            const bool box = __all_sync(0xFFFFFFFFu, my_row >= 0 && my_row == row0 + lane);
+            const float scale = a.scale ? a.scale[t.adapter] : 1.f;
             // ---- this block's share of t, to the rows' owners
             if (tiles > 0) ok = tc::mbar_wait_cluster(t_full, (tiles & 1u) ^ 1u, err);  // their inboxes are read
             if (ok && kb1 > kb0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
@@ -280,7 +340,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (!ok) break;
             tc::tc_fence_after();
             const uint32_t owner = static_cast<uint32_t>(tid / own_rows);
-            const uint32_t to = cluster_map(inbox + (q * own_rows + tid % own_rows) * r16 * 4u, owner);
+            const uint32_t to = cluster_map(inbox + (q * own_rows + tid % own_rows) * inbox_ld, owner);
             for (int c0 = 0; c0 < r16; c0 += 32) {
                 uint32_t v[32];
                 if (kb1 > kb0) {
@@ -292,7 +352,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)
-                    if (c0 + j < r16) st_cluster_v4(to + (c0 + j) * 4u, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if (c0 + j < r16) st_cluster_v4(to + ((((c0 + j) / 4) ^ (lane & inbox_mix)) << 4), v[j], v[j + 1], v[j + 2], v[j + 3]);
             }
             tc::tc_fence_before();
             fence_cluster();
@@ -307,7 +367,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             ok = tc::mbar_wait_cluster(inbox_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            const float scale = a.scale ? a.scale[t.adapter] : 1.f;
             const int per_row = r16 / 8;
             for (int e = tid; e < own_rows * per_row; e += 128) {
                 const int rr = e / per_row, c = e % per_row, m = static_cast<int>(q) * own_rows + rr;
@@ -315,18 +374,19 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = 0.f;
                 if (m < t.count) {
+#pragma unroll 4
                     for (uint32_t src = 0; src < cs; ++src) {
-                        const uint32_t at = inbox + ((src * own_rows + rr) * r16 + c * 8) * 4u;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float f[4];
-                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
-                                         : "r"(at + 16u * j)
-                                         : "memory");
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[4 * j + i] += f[i];
-                        }
+                        const float4* at = reinterpret_cast<const float4*>(
+                            smem_raw + (inbox - tc::smem_u32(smem_raw)) + (src * own_rows + rr) * inbox_ld);
+                        const float4 f0 = at[(2 * c) ^ (rr & inbox_mix)], f1 = at[(2 * c + 1) ^ (rr & inbox_mix)];
+                        v[0] += f0.x;
+                        v[1] += f0.y;
+                        v[2] += f0.z;
+                        v[3] += f0.w;
+                        v[4] += f1.x;
+                        v[5] += f1.y;
+                        v[6] += f1.z;
+                        v[7] += f1.w;
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = c * 8 + j < a.rank ? v[j] * scale : 0.f;
@@ -360,65 +420,76 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             // ---- out = base + the second product
             it += kb1 - kb0;
             s = it % slots;
+            int held = -1;  // slot that this warp's TMA store may still be reading
             for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
                 const int i = acc2 & 1;
                 ok = tc::mbar_wait(full(s), (it / slots) & 1u, err) && tc::mbar_wait(acc2_full(i), (acc2 >> 1) & 1u, err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const uint32_t line = slot_at(s) + tid * 128u;
+                uint8_t* tok = smem_raw + (slot_at(s) - tc::smem_u32(smem_raw)) + w4 * 4096;  // 32 rows of 128 bytes
+                uint32_t v[64];
+                const uint32_t d = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kAccCol + i * kStep;
+                tc::tmem_ld_32x32b_x32(d, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                tc::tmem_ld_32x32b_x32(d + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+                uint4 y[8];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t v[32];
-                    tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kAccCol + i * kStep + half * 32,
-                                           v);
-                    tc::tmem_wait_ld();
-                    if (my_row >= 0) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t at = line + (((half * 4 + c) ^ (lane & 7)) << 4);
-                            uint32_t y[4];
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                                         : "r"(at)
-                                         : "memory");
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                y[j] = pack_bf16(__uint_as_float(y[j] << 16) + __uint_as_float(v[c * 8 + 2 * j]),
-                                                 __uint_as_float(y[j] & 0xFFFF0000u) +
-                                                     __uint_as_float(v[c * 8 + 2 * j + 1]));
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]),
-                                         "r"(y[2]), "r"(y[3])
-                                         : "memory");
-                        }
-                    }
-                }
+                for (int c = 0; c < 8; ++c) y[c] = *reinterpret_cast<const uint4*>(tok + lane * 128 + ((c ^ (lane & 7)) << 4));
+                tc::tmem_wait_ld();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(acc2_empty(i));
-                // eight lanes store the 128 bytes of a row
-                const int64_t col = static_cast<int64_t>(b) * kStep + (lane & 7) * 8;
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const int m = g * 4 + (lane >> 3);
-                    const int row = __shfl_sync(0xFFFFFFFFu, my_row, m);
-                    if (row >= 0 && col < a.N) {
-                        uint4 y;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                                     : "r"(slot_at(s) + (w4 * 32 + m) * 128u + (((lane & 7) ^ (m & 7)) << 4))
-                                     : "memory");
-                        *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row) * a.N + col) = y;
-                    }
+                for (int c = 0; c < 8; ++c) {
+                    y[c].x = add_bf16x2(y[c].x, v[c * 8], v[c * 8 + 1]);
+                    y[c].y = add_bf16x2(y[c].y, v[c * 8 + 2], v[c * 8 + 3]);
+                    y[c].z = add_bf16x2(y[c].z, v[c * 8 + 4], v[c * 8 + 5]);
+                    y[c].w = add_bf16x2(y[c].w, v[c * 8 + 6], v[c * 8 + 7]);
                 }
-                tc::fence_proxy_async_smem();  // the slot is written by a TMA load next
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(free2(s));
+#pragma unroll
+                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tok + lane * 128 + ((c ^ (lane & 7)) << 4)) = y[c];
+                if (box) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_2d(&map_out, slot_at(s) + w4 * 4096u, b * kStep, row0);
+                        tc::bulk_commit_group();
+                        if (held >= 0) {
+                            tc::bulk_wait_group_read<1>();
+                            tc::mbar_arrive(free2(held));
+                        }
+                    }
+                    held = s;
+                } else {
+                    __syncwarp();
+                    // eight lanes store the 128 bytes of a row
+                    const int64_t col = static_cast<int64_t>(b) * kStep + (lane & 7) * 8;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        y[g] = *reinterpret_cast<const uint4*>(tok + (g * 4 + (lane >> 3)) * 128 +
+                                                               (((lane & 7) ^ ((g * 4 + (lane >> 3)) & 7)) << 4));
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const int row = __shfl_sync(0xFFFFFFFFu, my_row, g * 4 + (lane >> 3));
+                        if (row >= 0 && col < a.N)
+                            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row) * a.N + col) = y[g];
+                    }
+                    tc::fence_proxy_async_smem();  // the slot is written by a TMA load next
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(free2(s));
+                }
                 ++it;
                 if (++s == slots) s = 0;
             }
+            if (held >= 0 && lane == 0) {
+                tc::bulk_wait_group_read<0>();
+                tc::mbar_arrive(free2(held));
+            }
+            __syncwarp();
             ++tiles;
         }
+        if (lane == 0) tc::bulk_wait_group<0>();  // the stores have completed before the block ends
+        __syncwarp();
     }
 
     tc::tc_fence_before();
@@ -427,8 +498,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, kTmemColumns);
     }
-    cluster_arrive();  // no block of the cluster writes to this one's shared memory any more
-    cluster_wait();
+    if (cs > 1) {  // no block of the cluster writes to this one's shared memory any more
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 }  // namespace nq
@@ -468,18 +541,23 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     ua.r16 = (a.rank + 15) / 16 * 16;
     ua.panels = (a.rank + 63) / 64;
     ua.slot_bytes = nq::kTokBytes + static_cast<uint32_t>(ua.panels) * 8192u;
-    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + nq::kTok * ua.r16 * 4 +
+    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + nq::kTok * (ua.r16 * 4 + (ua.r16 % 32 == 0 ? 0 : 16)) +
                          8 * (3 * nq::kMaxSlots) + 80;
     ua.slots = static_cast<int>(std::min<size_t>(nq::kMaxSlots, (kUmmaSmemMax - fixed) / ua.slot_bytes));
     const size_t smem = fixed + ua.slots * static_cast<size_t>(ua.slot_bytes);
 
-    CUtensorMap mz, mbase, ma, mb;
-    const int gather_box[2] = {64, 1}, a_box[3] = {64, ua.r16, 1}, b_box[3] = {64, 64, 1};
+    CUtensorMap mz, mz1, mbase, mbase1, mout, ma, mb;
+    const int box[2] = {64, 32}, row_box[2] = {64, 1}, a_box[3] = {64, ua.r16, 1}, b_box[3] = {64, 64, 1};
     const int64_t z_dims[2] = {a.K, a.M}, base_dims[2] = {a.N, a.M};
     const int64_t a_dims[3] = {a.d_in, a.rank, a.n}, a_st[2] = {a.lda, a.lda * a.rank};
     const int64_t b_dims[3] = {a.rank, a.d_out, a.n}, b_st[2] = {a.ldb, a.ldb * a.d_out};
-    if (!tmap_bf16(&mz, a.z, 2, z_dims, &a.K, gather_box) ||
-        !tmap_bf16(&mbase, a.out ? a.base : a.z, 2, a.out ? base_dims : z_dims, a.out ? &a.N : &a.K, gather_box) ||
+    const bool second = a.out != nullptr;  // without it the second product's maps are not used
+    const uint16_t* base = second ? a.base : a.z;
+    const uint16_t* out = second ? a.out : a.z;
+    const int64_t* bd = second ? base_dims : z_dims;
+    if (!tmap_bf16(&mz, a.z, 2, z_dims, &a.K, box) || !tmap_bf16(&mz1, a.z, 2, z_dims, &a.K, row_box) ||
+        !tmap_bf16(&mbase, base, 2, bd, bd, box) || !tmap_bf16(&mbase1, base, 2, bd, bd, row_box) ||
+        !tmap_bf16(&mout, out, 2, bd, bd, box) ||
         !tmap_bf16(&ma, a.A, 3, a_dims, a_st, a_box) || !tmap_bf16(&mb, a.B, 3, b_dims, b_st, b_box))
         return NQ_ERR_LAUNCH;
 
@@ -503,7 +581,7 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     int cs = 8;
     while (cs > 1 && least * cs > sms) cs /= 2;
     const int64_t clusters = std::min(nq::max_adapter_tiles(a.M, a.n, nq::kTok), std::max<int64_t>(1, sms / cs));
-    void* kargs[] = {&mz, &mbase, &ma, &mb, &ua};
+    void* kargs[] = {&mz, &mz1, &mbase, &mbase1, &mout, &ma, &mb, &ua};
     return nq_host::launch_ex(fn, dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(cs)),
                               dim3(nq::kUmmaThreads), smem, stream, kargs, pdl, cs) == cudaSuccess
                ? NQ_OK
