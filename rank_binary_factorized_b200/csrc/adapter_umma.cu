@@ -29,7 +29,8 @@ namespace nq {
 constexpr int kTok = 128;                  // rows of a tile: the MMA's M
 constexpr int kStep = 64;                  // K or N elements of a slot
 constexpr uint32_t kTokBytes = kTok * 128; // 128 rows x 64 bf16
-constexpr int kUmmaThreads = 192;
+constexpr int kEpiWarps = 8;
+constexpr int kUmmaThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxSlots = 8;
 constexpr uint32_t kAccCol = 128;          // the second product's accumulators, 64 columns each
 constexpr uint32_t kTmemColumns = 256;
@@ -58,10 +59,20 @@ __device__ __forceinline__ float rest_of(float v, uint32_t part) {
     return isinf(p) ? 0.f : v - p;
 }
 
+// Two fp32 values as the sum of two bf16 values each.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(a, b);
+    lo = pack_bf16(rest_of(a, hi << 16), rest_of(b, hi & 0xFFFF0000u));
+}
+
+// Barrier of the epilogue's warps.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
+
 template <bool BWD>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
-    adapter_umma_kernel(const __grid_constant__ CUtensorMap map_z, const __grid_constant__ CUtensorMap map_z1,
-                        const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base1,
+    adapter_umma_kernel(const __grid_constant__ CUtensorMap map_z, const __grid_constant__ CUtensorMap map_z32,
+                        const __grid_constant__ CUtensorMap map_z1, const __grid_constant__ CUtensorMap map_base,
+                        const __grid_constant__ CUtensorMap map_base32, const __grid_constant__ CUtensorMap map_base1,
                         const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_a,
                         const __grid_constant__ CUtensorMap map_b, const AdapterUmmaArgs ua) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -72,11 +83,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const int own_rows = kTok / static_cast<int>(cs);  // rows of t that a block puts together
     const uint32_t part_bytes = static_cast<uint32_t>(panels) * kTokBytes;
     const uint32_t t_base = smem_base + slots * ua.slot_bytes;  // [2 parts][panels][128 rows][128 B], swizzled
-    const uint32_t inbox = t_base + 2 * part_bytes;             // [cs][own_rows][r16] fp32
-    // neighbouring rows of the inbox use different banks: their 16-byte pieces are permuted where a
-    // row fills whole 128-byte lines, else the rows are padded
-    const uint32_t inbox_mix = r16 % 32 == 0 ? 7u : 0u, inbox_ld = r16 * 4u + (inbox_mix ? 0u : 16u);
-    const uint32_t bars = inbox + kTok * inbox_ld;
+    // Partial t of the rows that this block owns: [cs blocks][segments of 32 ranks][row groups of 32 or
+    // own_rows][8 pieces of 4 ranks][rows of the group], 16 bytes a piece.  A warp of the epilogue
+    // writes and sends what it holds of a segment and group as one run.
+    const int segs = (r16 + 31) / 32, grp = min(own_rows, 32);
+    const uint32_t seg_bytes = own_rows * 128u;
+    const uint32_t inbox = t_base + 2 * part_bytes;
+    const uint32_t bars = inbox + segs * kTokBytes;
     auto slot_at = [&](int s) { return smem_base + s * ua.slot_bytes; };
     auto full = [&](int s) { return bars + 8u * s; };
     auto free1 = [&](int s) { return bars + 8u * (kMaxSlots + s); };      // first product: its MMAs are done
@@ -89,33 +102,34 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* err = a.err;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < slots; ++s) {
-            tc::mbar_init(full(s), 1);
-            tc::mbar_init(free1(s), 1);
-            tc::mbar_init(free2(s), 4);
+    if (warp == 0) {
+        if (lane < slots) {
+            tc::mbar_init(full(lane), 1);
+            tc::mbar_init(free1(lane), 1);
+            tc::mbar_init(free2(lane), 4);
+        } else if (lane == 8) {
+            tc::mbar_init(acc1_full, 1);
+            tc::mbar_init(acc1_empty, kEpiWarps);
+            tc::mbar_init(inbox_full, kEpiWarps);
+            tc::mbar_init(t_full, 1);
+            tc::mbar_init(drain, 1);
+        } else if (lane == 9 || lane == 10) {
+            tc::mbar_init(acc2_full(lane - 9), 1);
+            tc::mbar_init(acc2_empty(lane - 9), 4);
         }
-        tc::mbar_init(acc1_full, 1);
-        tc::mbar_init(acc1_empty, 4);
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(acc2_full(i), 1);
-            tc::mbar_init(acc2_empty(i), 4);
-        }
-        // every block sends the rows that this one owns, from the warps that hold them
-        tc::mbar_init(inbox_full, cs * static_cast<uint32_t>(max(1, own_rows / 32)));
-        tc::mbar_init(t_full, cs * 4u);
-        tc::mbar_init(drain, 1);
         tc::mbar_fence_init();
-        tc::tma_prefetch_desc(&map_z);
-        tc::tma_prefetch_desc(&map_a);
-        tc::tma_prefetch_desc(&map_b);
-        tc::tma_prefetch_desc(&map_base);
-        tc::tma_prefetch_desc(&map_out);
-    }
-    if (warp == 1) {
+        __syncwarp();
+    } else if (warp == 1) {
         tc::tmem_alloc(tmem_slot, kTmemColumns);
         tc::tmem_relinquish();
+    } else if (warp == 2 && tc::elect_one()) {
+        tc::tma_prefetch_desc(&map_z);
+        tc::tma_prefetch_desc(BWD ? &map_b : &map_a);
+        tc::tma_prefetch_desc(&map_base);
+        tc::tma_prefetch_desc(BWD ? &map_a : &map_b);
+        tc::tma_prefetch_desc(&map_out);
     }
+    __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
     // Waited for before another block's barriers are used, by each warp where it can afford to: with
@@ -155,8 +169,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (t.adapter < 0) break;
             if (t.adapter >= a.n) continue;
             // lane l holds entries 4 l .. 4 l + 3; eight lanes hold a group of 32 rows, which one TMA
-            // box fetches where the rows follow one another (it may fetch rows past the tile's last:
-            // they reach no output), and row gathers where they do not
+            // box fetches where the rows follow one another and over half of it is wanted (rows past the
+            // tile's last reach no output), and row gathers where not; one box takes a whole tile
             int32_t row[4];
             bool follow = true;
             const int first32 = __shfl_sync(0xFFFFFFFFu, 4 * lane < t.count ? a.rows[t.first + 4 * lane] : -1, lane & 24);
@@ -168,11 +182,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 row[i] = r >= 0 ? r : static_cast<int32_t>(a.M);  // past the last row: zeros
             }
             const bool used = 4 * lane < t.count;
-            const bool box = ((__ballot_sync(0xFFFFFFFFu, follow) >> (lane & 24)) & 0xFFu) == 0xFFu;
+            const bool box = ((__ballot_sync(0xFFFFFFFFu, follow) >> (lane & 24)) & 0xFFu) == 0xFFu &&
+                             t.count - 4 * (lane & 24) > 16;
             const bool loads = used && (!box || (lane & 7) == 0);
             uint32_t z_bytes = loads ? (box ? 4096u : 512u) : 0u;  // of all the lanes' loads
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) z_bytes += __shfl_xor_sync(0xFFFFFFFFu, z_bytes, o);
+            const int32_t tile_row0 = __shfl_sync(0xFFFFFFFFu, row[0], 0);
+            const bool whole = t.count > 112 && __all_sync(0xFFFFFFFFu, !used || (box && row[0] == tile_row0 + 4 * lane));  // one box
             bool boxes = true;  // every group that has rows is a box
             int32_t row0[4];
 #pragma unroll
@@ -184,24 +201,26 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 if (!next(second)) return false;
                 const uint32_t tok = slot_at(s), w = tok + kTokBytes, bar = full(s);
                 if (tc::elect_one()) {
-                    tc::mbar_arrive_expect_tx(bar, z_bytes + (second ? w2_bytes : w1_bytes));
+                    tc::mbar_arrive_expect_tx(bar, (whole ? kTokBytes : z_bytes) + (second ? w2_bytes : w1_bytes));
                     if (second == BWD) {  // A: [rank][64 of d_in]
                         tc::tma_load_3d(w, &map_a, b * kStep, 0, t.adapter, bar);
                     } else {  // B: [64 of d_out][rank], in panels of 64 ranks
                         for (int p = 0; p < panels; ++p)
                             tc::tma_load_3d(w + p * 8192u, &map_b, p * 64, b * kStep, t.adapter, bar);
                     }
-                    if (boxes) {
+                    if (whole) {
+                        tc::tma_load_2d(tok, second ? &map_base : &map_z, b * kStep, tile_row0, bar);
+                    } else if (boxes) {
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
                             if (32 * g < t.count)
-                                tc::tma_load_2d(tok + g * 4096u, second ? &map_base : &map_z, b * kStep, row0[g], bar);
+                                tc::tma_load_2d(tok + g * 4096u, second ? &map_base32 : &map_z32, b * kStep, row0[g], bar);
                     }
                 }
                 __syncwarp();
                 if (!boxes && loads) {
                     if (box)
-                        tc::tma_load_2d(tok + lane * 512u, second ? &map_base : &map_z, b * kStep, row[0], bar);
+                        tc::tma_load_2d(tok + lane * 512u, second ? &map_base32 : &map_z32, b * kStep, row[0], bar);
                     else
                         tc::tma_gather4(tok + lane * 512u, second ? &map_base1 : &map_z1, b * kStep, row, bar);
                 }
@@ -256,7 +275,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 }
             }
             if (ok && nb1 > nb0) {
-                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait_cluster(t_full, tiles & 1u, err));
+                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(t_full, tiles & 1u, err));
                 tc::fence_proxy_async_smem();  // t was written by threads
                 tc::tc_fence_after();
                 for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
@@ -298,26 +317,31 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         if (cs > 1) cluster_wait();
     } else {
         // ---------------------------------------------------------------- epilogue
-        const int w4 = warp & 3;  // TMEM lanes 32 w4 .. 32 w4 + 31
-        const int tid = w4 * 32 + lane;
+        // two sets of four warps take the column blocks in turn
+        const int w4 = warp & 3;         // TMEM lanes 32 w4 .. 32 w4 + 31
+        const int set = (warp - 2) / 4;
+        const int tid = w4 * 32 + lane;  // row of the tile
+        const int eid = threadIdx.x - 64;
         uint32_t it = 0, tiles = 0, acc2 = 0;
         int s = 0;
         bool ok = true;
         int tile = blockIdx.x;
         AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err), t_next;
         if (cs > 1) cluster_wait();  // every block's barriers are set up
-        for (; ok && t.adapter >= 0; t = t_next) {
+        // A warp whose wait gave up goes through the remaining tiles without work or waits: the others
+        // meet it at the barriers below.
+        for (; t.adapter >= 0; t = t_next) {
             tile += gridDim.x;
             t_next = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
             const int my_row = tid < t.count ? checked_row(a.rows, t.first + tid, a.M, err) : -1;
             if (t.adapter >= a.n) {
                 // rows without an adapter: t = 0, out = base (this block's columns)
-                if (a.t && q == 0 && my_row >= 0)
+                if (a.t && q == 0 && set == 0 && my_row >= 0)
                     for (int r = 0; r < a.rank; ++r) a.t[static_cast<int64_t>(my_row) * a.rank + r] = 0.f;
                 if (a.out && a.out != a.base) {
                     const int64_t c0 = static_cast<int64_t>(nb0) * kStep;
                     const int64_t c1 = min(a.N, static_cast<int64_t>(nb1) * kStep);
-                    for (int m = 0; m < 32; ++m) {
+                    for (int m = set; m < 32; m += 2) {
                         const int row = __shfl_sync(0xFFFFFFFFu, my_row, m);
                         if (row < 0) continue;
                         const uint16_t* src = a.base + static_cast<int64_t>(row) * a.N;
@@ -333,43 +357,58 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const int row0 = __shfl_sync(0xFFFFFFFFu, my_row, 0);
             const bool box = __all_sync(0xFFFFFFFFu, my_row >= 0 && my_row == row0 + lane);
             const float scale = a.scale ? a.scale[t.adapter] : 1.f;
-            // ---- this block's share of t, to the rows' owners
-            if (tiles > 0) ok = tc::mbar_wait_cluster(t_full, (tiles & 1u) ^ 1u, err);  // their inboxes are read
+            // ---- this block's share of t, to the rows' owners.  It is put where the owner's rows of t
+            // will arrive: t_full of the last tile said that the owners have read their inboxes and
+            // that the old t is here, the barrier below that every warp is done with it.
+            if (tiles > 0) {
+                ok = ok && tc::mbar_wait(t_full, (tiles & 1u) ^ 1u, err);
+                epilogue_sync();
+            }
             if (ok && kb1 > kb0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t owner = static_cast<uint32_t>(tid / own_rows);
-            const uint32_t to = cluster_map(inbox + (q * own_rows + tid % own_rows) * inbox_ld, owner);
-            for (int c0 = 0; c0 < r16; c0 += 32) {
+            const uint32_t owner = static_cast<uint32_t>(tid / own_rows), rl = tid % own_rows;
+            for (int g = set; g < segs && ok; g += 2) {
                 uint32_t v[32];
                 if (kb1 > kb0) {
-                    tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + c0, v);
+                    tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + g * 32, v);
                     tc::tmem_wait_ld();
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
+                const int pieces = min(8, (r16 - g * 32) / 4);
+                const uint32_t at = rl / grp * (grp * 128u);  // of the group in the segment
+                const uint32_t home = owner == q ? inbox + (q * segs + g) * seg_bytes : t_base + g * kTokBytes + owner * seg_bytes;
+                uint4* to = reinterpret_cast<uint4*>(smem_raw + (home + at - tc::smem_u32(smem_raw))) + rl % grp;
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    if (c0 + j < r16) st_cluster_v4(to + ((((c0 + j) / 4) ^ (lane & inbox_mix)) << 4), v[j], v[j + 1], v[j + 2], v[j + 3]);
+                for (int j = 0; j < 8; ++j)
+                    if (j < pieces) to[j * grp] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                for (int o = 0; o < 32; o += grp) {
+                    const uint32_t own = __shfl_sync(0xFFFFFFFFu, owner, o), src = __shfl_sync(0xFFFFFFFFu, home + at, o);
+                    const uint32_t off = __shfl_sync(0xFFFFFFFFu, at, o);
+                    if (own != q && tc::elect_one())
+                        tc::bulk_copy_cluster(cluster_map(inbox + (q * segs + g) * seg_bytes + off, own), src,
+                                              pieces * grp * 16u, cluster_map(inbox_full, own));
+                    __syncwarp();
+                }
             }
             tc::tc_fence_before();
-            fence_cluster();
             __syncwarp();
-            if (lane == 0 && kb1 > kb0) tc::mbar_arrive(acc1_empty);
-            if (own_rows >= 32) {
-                if (lane == 0) tc::mbar_arrive_cluster(cluster_map(inbox_full, owner));
-            } else if (lane % own_rows == 0) {
-                tc::mbar_arrive_cluster(cluster_map(inbox_full, owner));
+            if (lane == 0) {
+                if (kb1 > kb0) tc::mbar_arrive(acc1_empty);
+                if (eid == 0)
+                    tc::mbar_arrive_expect_tx(inbox_full, (cs - 1) * own_rows * r16 * 4u);
+                else
+                    tc::mbar_arrive(inbox_full);
             }
             // ---- the rows this block owns
-            ok = tc::mbar_wait_cluster(inbox_full, tiles & 1u, err);
+            ok = ok && tc::mbar_wait(inbox_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            const int per_row = r16 / 8;
-            for (int e = tid; e < own_rows * per_row; e += 128) {
-                const int rr = e / per_row, c = e % per_row, m = static_cast<int>(q) * own_rows + rr;
+            for (int e = eid; e < own_rows * (r16 / 8) && ok; e += 32 * kEpiWarps) {
+                const int rr = e % own_rows, c = e / own_rows, m = static_cast<int>(q) * own_rows + rr;
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -377,8 +416,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll 4
                     for (uint32_t src = 0; src < cs; ++src) {
                         const float4* at = reinterpret_cast<const float4*>(
-                            smem_raw + (inbox - tc::smem_u32(smem_raw)) + (src * own_rows + rr) * inbox_ld);
-                        const float4 f0 = at[(2 * c) ^ (rr & inbox_mix)], f1 = at[(2 * c + 1) ^ (rr & inbox_mix)];
+                            smem_raw + (inbox + (src * segs + c / 4) * seg_bytes + rr / grp * (grp * 128u) -
+                                        tc::smem_u32(smem_raw))) + rr % grp;
+                        const float4 f0 = at[c % 4 * 2 * grp], f1 = at[(c % 4 * 2 + 1) * grp];
                         v[0] += f0.x;
                         v[1] += f0.y;
                         v[2] += f0.z;
@@ -399,30 +439,38 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         }
                     }
                 }
-                if (!a.out) continue;
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hi[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                    lo[j] = pack_bf16(rest_of(v[2 * j], hi[j] << 16), rest_of(v[2 * j + 1], hi[j] & 0xFFFF0000u));
-                }
-                const uint32_t at = t_base + (c / 8) * kTokBytes + m * 128u + (((c % 8) ^ (m & 7)) << 4);
-                for (uint32_t dst = 0; dst < cs; ++dst) {
-                    const uint32_t remote = cluster_map(at, dst);
-                    st_cluster_v4(remote, hi[0], hi[1], hi[2], hi[3]);
-                    st_cluster_v4(remote + part_bytes, lo[0], lo[1], lo[2], lo[3]);
+                uint4 hi, lo;
+                split_bf16(v[0], v[1], hi.x, lo.x);
+                split_bf16(v[2], v[3], hi.y, lo.y);
+                split_bf16(v[4], v[5], hi.z, lo.z);
+                split_bf16(v[6], v[7], hi.w, lo.w);
+                uint8_t* at = smem_raw + (t_base - tc::smem_u32(smem_raw)) + (c / 8) * kTokBytes + m * 128 +
+                              (((c % 8) ^ (m & 7)) << 4);
+                *reinterpret_cast<uint4*>(at) = hi;
+                *reinterpret_cast<uint4*>(at + part_bytes) = lo;
+            }
+            tc::fence_proxy_async_smem();  // the copies and the tensor cores read t
+            epilogue_sync();
+            if (ok && eid / 32 < static_cast<int>(cs) && static_cast<uint32_t>(eid / 32) != q && tc::elect_one()) {
+                const uint32_t bar = cluster_map(t_full, eid / 32);
+                for (int g = 0; g < 2 * panels; ++g) {
+                    const uint32_t at = t_base + g * kTokBytes + q * seg_bytes;
+                    tc::bulk_copy_cluster(cluster_map(at, eid / 32), at, seg_bytes, bar);
                 }
             }
-            asm volatile("fence.proxy.async;" ::: "memory");  // the tensor cores read t
-            fence_cluster();
             __syncwarp();
-            if (lane < static_cast<int>(cs)) tc::mbar_arrive_cluster(cluster_map(t_full, lane));
+            if (eid == 0) tc::mbar_arrive_expect_tx(t_full, (cs - 1) * 2 * panels * seg_bytes);
             // ---- out = base + the second product
             it += kb1 - kb0;
             s = it % slots;
             int held = -1;  // slot that this warp's TMA store may still be reading
             for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
                 const int i = acc2 & 1;
+                if (i != set) {
+                    ++it;
+                    if (++s == slots) s = 0;
+                    continue;
+                }
                 ok = tc::mbar_wait(full(s), (it / slots) & 1u, err) && tc::mbar_wait(acc2_full(i), (acc2 >> 1) & 1u, err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -458,8 +506,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                             tc::bulk_wait_group_read<1>();
                             tc::mbar_arrive(free2(held));
                         }
+                        if (slots < 6) {  // too few to leave this one for later
+                            tc::bulk_wait_group_read<0>();
+                            tc::mbar_arrive(free2(s));
+                        }
                     }
-                    held = s;
+                    held = slots < 6 ? -1 : s;
                 } else {
                     __syncwarp();
                     // eight lanes store the 128 bytes of a row
@@ -488,7 +540,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             __syncwarp();
             ++tiles;
         }
-        if (lane == 0) tc::bulk_wait_group<0>();  // the stores have completed before the block ends
+        // t of the last tile has arrived and the stores have completed before the block ends
+        if (tiles > 0) tc::mbar_wait(t_full, (tiles & 1u) ^ 1u, err);
+        if (lane == 0) tc::bulk_wait_group<0>();
         __syncwarp();
     }
 
@@ -530,6 +584,36 @@ bool tmap_bf16(CUtensorMap* map, const void* base, int dims, const int64_t* exte
 
 }  // namespace
 
+namespace {
+
+// Clusters of cs blocks of the kernel that fit on the device at once (one block a multiprocessor).
+int resident_clusters(int dev, int cs) {
+    static std::atomic<int> known[64][4];
+    std::atomic<int>& slot = known[dev][cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0];
+    int n = slot.load(std::memory_order_acquire);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1, static_cast<unsigned>(cs));
+        cfg.blockDim = dim3(nq::kUmmaThreads);
+        cfg.dynamicSmemBytes = kUmmaSmemMax;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1;
+        attr[0].val.clusterDim.y = static_cast<unsigned>(cs);
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, nq::adapter_umma_kernel<false>, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = std::max(1, nq_host::sm_count() / (2 * cs));  // unknown: assume half
+        }
+        slot.store(n, std::memory_order_release);
+    }
+    return n;
+}
+
+}  // namespace
+
 // Every row of z, base, A and B starts on 16 bytes, as TMA needs.
 bool nq_adapter_umma_fits(const nq::AdapterArgs& a) {
     return a.K % 8 == 0 && a.N % 8 == 0 && a.lda % 8 == 0 && a.ldb % 8 == 0;
@@ -541,13 +625,14 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     ua.r16 = (a.rank + 15) / 16 * 16;
     ua.panels = (a.rank + 63) / 64;
     ua.slot_bytes = nq::kTokBytes + static_cast<uint32_t>(ua.panels) * 8192u;
-    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + nq::kTok * (ua.r16 * 4 + (ua.r16 % 32 == 0 ? 0 : 16)) +
+    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + (ua.r16 + 31) / 32 * static_cast<size_t>(nq::kTokBytes) +
                          8 * (3 * nq::kMaxSlots) + 80;
     ua.slots = static_cast<int>(std::min<size_t>(nq::kMaxSlots, (kUmmaSmemMax - fixed) / ua.slot_bytes));
     const size_t smem = fixed + ua.slots * static_cast<size_t>(ua.slot_bytes);
 
-    CUtensorMap mz, mz1, mbase, mbase1, mout, ma, mb;
-    const int box[2] = {64, 32}, row_box[2] = {64, 1}, a_box[3] = {64, ua.r16, 1}, b_box[3] = {64, 64, 1};
+    CUtensorMap mz, mz32, mz1, mbase, mbase32, mbase1, mout, ma, mb;
+    const int box[2] = {64, nq::kTok}, box32[2] = {64, 32}, row_box[2] = {64, 1};
+    const int a_box[3] = {64, ua.r16, 1}, b_box[3] = {64, 64, 1};
     const int64_t z_dims[2] = {a.K, a.M}, base_dims[2] = {a.N, a.M};
     const int64_t a_dims[3] = {a.d_in, a.rank, a.n}, a_st[2] = {a.lda, a.lda * a.rank};
     const int64_t b_dims[3] = {a.rank, a.d_out, a.n}, b_st[2] = {a.ldb, a.ldb * a.d_out};
@@ -555,9 +640,10 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     const uint16_t* base = second ? a.base : a.z;
     const uint16_t* out = second ? a.out : a.z;
     const int64_t* bd = second ? base_dims : z_dims;
-    if (!tmap_bf16(&mz, a.z, 2, z_dims, &a.K, box) || !tmap_bf16(&mz1, a.z, 2, z_dims, &a.K, row_box) ||
-        !tmap_bf16(&mbase, base, 2, bd, bd, box) || !tmap_bf16(&mbase1, base, 2, bd, bd, row_box) ||
-        !tmap_bf16(&mout, out, 2, bd, bd, box) ||
+    if (!tmap_bf16(&mz, a.z, 2, z_dims, &a.K, box) || !tmap_bf16(&mz32, a.z, 2, z_dims, &a.K, box32) ||
+        !tmap_bf16(&mz1, a.z, 2, z_dims, &a.K, row_box) || !tmap_bf16(&mbase, base, 2, bd, bd, box) ||
+        !tmap_bf16(&mbase32, base, 2, bd, bd, box32) || !tmap_bf16(&mbase1, base, 2, bd, bd, row_box) ||
+        !tmap_bf16(&mout, out, 2, bd, bd, box32) ||
         !tmap_bf16(&ma, a.A, 3, a_dims, a_st, a_box) || !tmap_bf16(&mb, a.B, 3, b_dims, b_st, b_box))
         return NQ_ERR_LAUNCH;
 
@@ -575,13 +661,14 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
                 return NQ_ERR_LAUNCH;
         attr_done[dev].store(true, std::memory_order_release);
     }
-    // The fewest tiles that M rows can make decide how many blocks share one (at most a portable
-    // cluster); clusters loop over the tiles that a finer grouping adds.
-    const int64_t sms = nq_host::sm_count(), least = (a.M + nq::kTok - 1) / nq::kTok;
+    // The fewest tiles that M rows can make decide how many blocks share one: as many as a portable
+    // cluster has while every tile's cluster is resident at once.  Clusters loop over the tiles that
+    // a finer grouping adds.
+    const int64_t least = (a.M + nq::kTok - 1) / nq::kTok;
     int cs = 8;
-    while (cs > 1 && least * cs > sms) cs /= 2;
-    const int64_t clusters = std::min(nq::max_adapter_tiles(a.M, a.n, nq::kTok), std::max<int64_t>(1, sms / cs));
-    void* kargs[] = {&mz, &mz1, &mbase, &mbase1, &mout, &ma, &mb, &ua};
+    while (cs > 1 && least > resident_clusters(dev, cs)) cs /= 2;
+    const int64_t clusters = std::min<int64_t>(nq::max_adapter_tiles(a.M, a.n, nq::kTok), resident_clusters(dev, cs));
+    void* kargs[] = {&mz, &mz32, &mz1, &mbase, &mbase32, &mbase1, &mout, &ma, &mb, &ua};
     return nq_host::launch_ex(fn, dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(cs)),
                               dim3(nq::kUmmaThreads), smem, stream, kargs, pdl, cs) == cudaSuccess
                ? NQ_OK

@@ -82,35 +82,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
     return mbar_wait_for(bar, parity, err, kWaitLimitNs);
 }
 
-// The same for a barrier that other blocks of the cluster arrive on: their earlier writes to this
-// block's shared memory are visible once it returns true.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned int* err) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((i & 255u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
-            flag_error(err, kErrTimeout);
-            return false;
-        }
-    }
-}
-// Arrives on the barrier at the shared::cluster address `bar` (mapa of another block's barrier).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // ------------------------------------------------------------------ TMA (tile mode, one CTA per copy)
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -139,6 +110,14 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         "%4, %5, %6}], [%7];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
         : "memory");
+}
+
+// `bytes` of this block's shared memory to the shared::cluster address `dst`, counted by the
+// barrier `bar` of the same block of the cluster (addresses and size in multiples of 16).
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // Tile store shared::cta -> global through the tensor map (elements outside the tensor's
@@ -261,11 +240,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t remote) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t remote, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 }  // namespace nq
 
 // Host: the driver's cuTensorMapEncodeTiled (nullptr when unavailable), defined in prefill.cu.
