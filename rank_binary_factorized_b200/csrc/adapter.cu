@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kRowsThreads) adapter_rows_kernel(const Adapte
     pdl_wait();
     pdl_launch_dependents();
     if (threadIdx.x < 32) {
-        const AdapterTile t = find_tile(a.offsets, a.n, a.M, kRowsTile, static_cast<int>(blockIdx.x), a.err);
+        const AdapterTile t = find_tile(a.offsets, a.n, a.M, kRowsTile, kRowsTile, static_cast<int>(blockIdx.x),
+                                        a.err);
         if (threadIdx.x == 0) s.tile = t;
         if (threadIdx.x < kRowsTile)
             s.row[threadIdx.x] = static_cast<int>(threadIdx.x) < t.count
@@ -403,7 +404,7 @@ nq_status nq_launch_adapter_rows(const nq::AdapterArgs& a, bool backward, cudaSt
                 return NQ_ERR_LAUNCH;
         attr_done[dev].store(true, std::memory_order_release);
     }
-    const int64_t tiles = nq::max_adapter_tiles(a.M, a.n, nq::kRowsTile);
+    const int64_t tiles = nq::max_adapter_tiles(a.M, a.n, nq::kRowsTile, nq::kRowsTile);
     // blocks per tile: enough to give every multiprocessor one, at most a portable cluster
     int cs = 8;
     while (cs > 1 && tiles * cs > 2 * static_cast<int64_t>(nq_host::sm_count())) cs /= 2;

@@ -60,17 +60,19 @@ __device__ __forceinline__ void adapter_bounds(const int32_t* offsets, int n, in
     last = static_cast<int>(ok ? hi : 0);
 }
 
-// Tile number `tile` when every group's rows are cut into tiles of rows_per_tile, groups in
-// order.  A whole warp calls it; 32 groups are scanned at a time.
-__device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, int64_t M, int rows_per_tile, int tile,
-                                                 unsigned int* err) {
+// Tile number `tile` when every adapter's rows are cut into tiles of rows_per_tile and those
+// without one into tiles of none_per_tile, groups in order.  A whole warp calls it; 32 groups are
+// scanned at a time.
+__device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, int64_t M, int rows_per_tile,
+                                                 int none_per_tile, int tile, unsigned int* err) {
     const int lane = threadIdx.x & 31;
     int before = 0;  // tiles of the groups before this batch of 32
     for (int a0 = 0; a0 <= n; a0 += 32) {
         const int a = a0 + lane;
         int first = 0, last = 0;
         if (a <= n) adapter_bounds(offsets, n, M, a, first, last, err);
-        const int mine = (last - first + rows_per_tile - 1) / rows_per_tile;
+        const int per = a < n ? rows_per_tile : none_per_tile;
+        const int mine = (last - first + per - 1) / per;
         int upto = mine;  // inclusive sum over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -84,9 +86,9 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
             AdapterTile t;
             t.adapter = a0 + src;
             const int off = (local - (__shfl_sync(0xFFFFFFFFu, upto, src) - __shfl_sync(0xFFFFFFFFu, mine, src))) *
-                            rows_per_tile;
+                            (t.adapter < n ? rows_per_tile : none_per_tile);
             t.first = __shfl_sync(0xFFFFFFFFu, first, src) + off;
-            t.count = min(rows_per_tile, __shfl_sync(0xFFFFFFFFu, last, src) - t.first);
+            t.count = min(t.adapter < n ? rows_per_tile : none_per_tile, __shfl_sync(0xFFFFFFFFu, last, src) - t.first);
             return t;
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -94,10 +96,12 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
     return {-1, 0, 0};
 }
 
-// Upper bound of the number of tiles for any grouping of M rows into n adapters and "none".
-inline int64_t max_adapter_tiles(int64_t M, int64_t n, int rows_per_tile) {
+// Upper bound of the number of tiles for any grouping of M rows into n adapters and "none"
+// (none_per_tile <= rows_per_tile).
+inline int64_t max_adapter_tiles(int64_t M, int64_t n, int rows_per_tile, int none_per_tile) {
     const int64_t groups = n + 1 < M ? n + 1 : M;
-    return (M - groups) / rows_per_tile + groups;
+    const int64_t listed = (M - groups) / rows_per_tile + groups, none = (M - 1) / none_per_tile + 1;
+    return listed > none ? listed : none;
 }
 
 // Entry i of `rows`, or -1 (reported) when it is not a row.

@@ -20,6 +20,7 @@
 // - The epilogue adds the accumulator to the tile of base in shared memory and stores whole row pieces.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "adapter.cuh"
 #include "tc_common.cuh"
@@ -27,6 +28,7 @@
 namespace nq {
 
 constexpr int kTok = 128;                  // rows of a tile: the MMA's M
+constexpr int kNoneTok = 16;               // rows without an adapter in a tile: only copied
 constexpr int kStep = 64;                  // K or N elements of a slot
 constexpr uint32_t kTokBytes = kTok * 128; // 128 rows x 64 bf16
 constexpr int kEpiWarps = 8;
@@ -41,6 +43,7 @@ struct AdapterUmmaArgs {
     uint32_t slot_bytes;
     int panels;   // 64-element panels of the rank
     int r16;      // rank rounded up to the MMA's K
+    int own_shift; // log2(128 / blocks of the cluster)
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -68,6 +71,11 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
 // Barrier of the epilogue's warps.
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
 
+// Of `segs` segments of partial t; at least a tile of out for every warp of the epilogue.
+__host__ __device__ constexpr uint32_t inbox_bytes(int segs) {
+    return segs * kTokBytes > kEpiWarps * 4096u ? segs * kTokBytes : kEpiWarps * 4096u;
+}
+
 template <bool BWD>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
     adapter_umma_kernel(const __grid_constant__ CUtensorMap map_z, const __grid_constant__ CUtensorMap map_z32,
@@ -80,16 +88,17 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t smem_base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
     const int slots = ua.slots, panels = ua.panels, r16 = ua.r16;
     const uint32_t cs = cluster_nctarank(), q = cluster_ctarank();
-    const int own_rows = kTok / static_cast<int>(cs);  // rows of t that a block puts together
+    const int own_shift = ua.own_shift, own_rows = 1 << own_shift;  // rows of t that a block puts together
     const uint32_t part_bytes = static_cast<uint32_t>(panels) * kTokBytes;
     const uint32_t t_base = smem_base + slots * ua.slot_bytes;  // [2 parts][panels][128 rows][128 B], swizzled
     // Partial t of the rows that this block owns: [cs blocks][segments of 32 ranks][row groups of 32 or
     // own_rows][8 pieces of 4 ranks][rows of the group], 16 bytes a piece.  A warp of the epilogue
     // writes and sends what it holds of a segment and group as one run.
-    const int segs = (r16 + 31) / 32, grp = min(own_rows, 32);
+    const int segs = (r16 + 31) / 32, grp_shift = min(own_shift, 5), grp = 1 << grp_shift;
     const uint32_t seg_bytes = own_rows * 128u;
     const uint32_t inbox = t_base + 2 * part_bytes;
-    const uint32_t bars = inbox + segs * kTokBytes;
+    const uint32_t staging = inbox;  // between two tiles' t: the epilogue's tiles of out, 4 KB a warp
+    const uint32_t bars = inbox + inbox_bytes(segs);
     auto slot_at = [&](int s) { return smem_base + s * ua.slot_bytes; };
     auto full = [&](int s) { return bars + 8u * s; };
     auto free1 = [&](int s) { return bars + 8u * (kMaxSlots + s); };      // first product: its MMAs are done
@@ -98,7 +107,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     auto acc2_full = [&](int i) { return acc1_full + 16u + 8u * i; };
     auto acc2_empty = [&](int i) { return acc1_full + 32u + 8u * i; };
     const uint32_t inbox_full = acc1_full + 48u, t_full = acc1_full + 56u, drain = acc1_full + 64u;
-    const uint32_t tmem_slot = acc1_full + 72u;
+    const uint32_t peers_ready = acc1_full + 72u, tmem_slot = acc1_full + 80u;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* err = a.err;
@@ -112,6 +121,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             tc::mbar_init(acc1_empty, kEpiWarps);
             tc::mbar_init(inbox_full, kEpiWarps);
             tc::mbar_init(t_full, 1);
+            tc::mbar_init(peers_ready, cs);
             tc::mbar_init(drain, 1);
         } else if (lane == 9 || lane == 10) {
             tc::mbar_init(acc2_full(lane - 9), 1);
@@ -134,15 +144,16 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     __syncthreads();
     // Waited for before another block's barriers are used, by each warp where it can afford to: with
     // one block and no cluster launch, a wait by some of the warps did not return before the others'.
-    if (cs > 1) cluster_arrive();
+    if (cs > 1) cluster_arrive_relaxed();  // the barriers' own fence orders their set-up
     tc::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
 
     const int kb_all = static_cast<int>((a.K + kStep - 1) / kStep), nb_all = static_cast<int>((a.N + kStep - 1) / kStep);
-    const int kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * q / cs);
-    const int kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (q + 1) / cs);
-    const int nb0 = a.out ? static_cast<int>(static_cast<int64_t>(nb_all) * q / cs) : 0;
-    const int nb1 = a.out ? static_cast<int>(static_cast<int64_t>(nb_all) * (q + 1) / cs) : 0;
+    const int cs_shift = 7 - own_shift;  // cs = 1 << cs_shift
+    const int kb0 = static_cast<int>((static_cast<int64_t>(kb_all) * q) >> cs_shift);
+    const int kb1 = static_cast<int>((static_cast<int64_t>(kb_all) * (q + 1)) >> cs_shift);
+    const int nb0 = a.out ? static_cast<int>((static_cast<int64_t>(nb_all) * q) >> cs_shift) : 0;
+    const int nb1 = a.out ? static_cast<int>((static_cast<int64_t>(nb_all) * (q + 1)) >> cs_shift) : 0;
     const uint32_t w1_bytes = BWD ? panels * 8192u : r16 * 128u;
     const uint32_t w2_bytes = BWD ? r16 * 128u : panels * 8192u;
     pdl_wait();
@@ -154,18 +165,24 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         int s = 0;
         bool ok = true;
         auto next = [&](bool second) {  // waits until slot s may be written
+            const uint32_t bit = 1u << s;
             if (it >= static_cast<uint32_t>(slots)) {
-                const uint32_t bit = 1u << s;
-                if (lane == 0) ok = (was2 & bit) ? tc::mbar_wait(free2(s), (ph2 >> s) & 1u, err)
-                                                 : tc::mbar_wait(free1(s), (ph1 >> s) & 1u, err);
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                if (was2 & bit) ph2 ^= bit; else ph1 ^= bit;
+                if (was2 & bit) {
+                    ok = tc::mbar_wait(free2(s), (ph2 >> s) & 1u, err);
+                    ph2 ^= bit;
+                } else {
+                    ok = tc::mbar_wait(free1(s), (ph1 >> s) & 1u, err);
+                    ph1 ^= bit;
+                }
             }
-            was2 = second ? was2 | (1u << s) : was2 & ~(1u << s);
-            return ok;
+            was2 = second ? was2 | bit : was2 & ~bit;
+        };
+        auto advance = [&] {
+            ++it;
+            if (++s == slots) s = 0;
         };
         for (int tile = blockIdx.x; ok; tile += gridDim.x) {
-            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
+            const AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, kNoneTok, tile, err);
             if (t.adapter < 0) break;
             if (t.adapter >= a.n) continue;
             // lane l holds entries 4 l .. 4 l + 3; eight lanes hold a group of 32 rows, which one TMA
@@ -182,54 +199,83 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 row[i] = r >= 0 ? r : static_cast<int32_t>(a.M);  // past the last row: zeros
             }
             const bool used = 4 * lane < t.count;
-            const bool box = ((__ballot_sync(0xFFFFFFFFu, follow) >> (lane & 24)) & 0xFFu) == 0xFFu &&
-                             t.count - 4 * (lane & 24) > 16;
-            const bool loads = used && (!box || (lane & 7) == 0);
-            uint32_t z_bytes = loads ? (box ? 4096u : 512u) : 0u;  // of all the lanes' loads
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) z_bytes += __shfl_xor_sync(0xFFFFFFFFu, z_bytes, o);
+            const uint32_t follows = __ballot_sync(0xFFFFFFFFu, follow);
+            const bool box = ((follows >> (lane & 24)) & 0xFFu) == 0xFFu && t.count - 4 * (lane & 24) > 16;
             const int32_t tile_row0 = __shfl_sync(0xFFFFFFFFu, row[0], 0);
-            const bool whole = t.count > 112 && __all_sync(0xFFFFFFFFu, !used || (box && row[0] == tile_row0 + 4 * lane));  // one box
-            bool boxes = true;  // every group that has rows is a box
+            const bool whole = t.count > 112 && __all_sync(0xFFFFFFFFu, !used || (box && row[0] == tile_row0 + 4 * lane));
+            const bool loads = used && (!box || (lane & 7) == 0);
+            const uint32_t z_bytes = 4096u * __popc(__ballot_sync(0xFFFFFFFFu, loads && box)) +
+                                     512u * __popc(__ballot_sync(0xFFFFFFFFu, loads && !box));
+            const bool boxes = whole || __all_sync(0xFFFFFFFFu, !used || box);
             int32_t row0[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                row0[g] = __shfl_sync(0xFFFFFFFFu, row[0], 8 * g);
-                boxes = boxes && (__shfl_sync(0xFFFFFFFFu, box || !used, 8 * g) != 0);
-            }
-            auto load = [&](bool second, int b) {
-                if (!next(second)) return false;
-                const uint32_t tok = slot_at(s), w = tok + kTokBytes, bar = full(s);
-                if (tc::elect_one()) {
-                    tc::mbar_arrive_expect_tx(bar, (whole ? kTokBytes : z_bytes) + (second ? w2_bytes : w1_bytes));
-                    if (second == BWD) {  // A: [rank][64 of d_in]
-                        tc::tma_load_3d(w, &map_a, b * kStep, 0, t.adapter, bar);
-                    } else {  // B: [64 of d_out][rank], in panels of 64 ranks
-                        for (int p = 0; p < panels; ++p)
-                            tc::tma_load_3d(w + p * 8192u, &map_b, p * 64, b * kStep, t.adapter, bar);
-                    }
-                    if (whole) {
-                        tc::tma_load_2d(tok, second ? &map_base : &map_z, b * kStep, tile_row0, bar);
-                    } else if (boxes) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (32 * g < t.count)
-                                tc::tma_load_2d(tok + g * 4096u, second ? &map_base32 : &map_z32, b * kStep, row0[g], bar);
-                    }
+            for (int g = 0; g < 4; ++g) row0[g] = __shfl_sync(0xFFFFFFFFu, row[0], 8 * g);
+            // the tile of P or Q that goes with column block b, by one thread
+            auto load_w = [&](auto second, int b, uint32_t w, uint32_t bar) {
+                if constexpr (second.value == BWD) {  // A: [rank][64 of d_in]
+                    tc::tma_load_3d(w, &map_a, b * kStep, 0, t.adapter, bar);
+                } else {  // B: [64 of d_out][rank], in panels of 64 ranks
+                    tc::tma_load_3d(w, &map_b, 0, b * kStep, t.adapter, bar);
+                    if (panels > 1) tc::tma_load_3d(w + 8192u, &map_b, 64, b * kStep, t.adapter, bar);
                 }
-                __syncwarp();
-                if (!boxes && loads) {
-                    if (box)
-                        tc::tma_load_2d(tok + lane * 512u, second ? &map_base32 : &map_z32, b * kStep, row[0], bar);
-                    else
-                        tc::tma_gather4(tok + lane * 512u, second ? &map_base1 : &map_z1, b * kStep, row, bar);
-                }
-                ++it;
-                if (++s == slots) s = 0;
-                return true;
             };
-            for (int b = kb0; b < kb1 && ok; ++b) ok = load(false, b);
-            for (int b = nb0; b < nb1 && ok; ++b) ok = load(true, b);
+            auto load_all = [&](auto second, int b0, int b1) {
+                constexpr bool kSecond = second.value;
+                const CUtensorMap* box_map = kSecond ? &map_base : &map_z;
+                const CUtensorMap* box32_map = kSecond ? &map_base32 : &map_z32;
+                const CUtensorMap* row_map = kSecond ? &map_base1 : &map_z1;
+                const uint32_t bytes = (whole ? kTokBytes : z_bytes) + (kSecond ? w2_bytes : w1_bytes);
+                if (boxes) {
+                    const bool me = tc::elect_one();
+                    if (me) {
+                        for (int b = b0; b < b1; ++b) {
+                            next(kSecond);
+                            if (!ok) break;
+                            const uint32_t tok = slot_at(s), bar = full(s);
+                            tc::mbar_arrive_expect_tx(bar, bytes);
+                            if (whole) {
+                                tc::tma_load_2d(tok, box_map, b * kStep, tile_row0, bar);
+                            } else {
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    if (32 * g < t.count)
+                                        tc::tma_load_2d(tok + g * 4096u, box32_map, b * kStep, row0[g], bar);
+                            }
+                            load_w(second, b, tok + kTokBytes, bar);
+                            advance();
+                        }
+                    }
+                    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1;  // the state goes to every lane
+                    it = __shfl_sync(0xFFFFFFFFu, it, src);
+                    s = __shfl_sync(0xFFFFFFFFu, s, src);
+                    was2 = __shfl_sync(0xFFFFFFFFu, was2, src);
+                    ph1 = __shfl_sync(0xFFFFFFFFu, ph1, src);
+                    ph2 = __shfl_sync(0xFFFFFFFFu, ph2, src);
+                    ok = __shfl_sync(0xFFFFFFFFu, ok, src);
+                } else {
+                    for (int b = b0; b < b1; ++b) {
+                        next(kSecond);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        const uint32_t tok = slot_at(s), bar = full(s);
+                        if (tc::elect_one()) {
+                            tc::mbar_arrive_expect_tx(bar, bytes);
+                            load_w(second, b, tok + kTokBytes, bar);
+                        }
+                        __syncwarp();
+                        if (loads) {
+                            if (box)
+                                tc::tma_load_2d(tok + lane * 512u, box32_map, b * kStep, row[0], bar);
+                            else
+                                tc::tma_gather4(tok + lane * 512u, row_map, b * kStep, row, bar);
+                        }
+                        __syncwarp();
+                        advance();
+                    }
+                }
+            };
+            load_all(std::false_type{}, kb0, kb1);
+            if (ok) load_all(std::true_type{}, nb0, nb1);
         }
         // every load issued has landed before the block may end
         if (lane == 0) {
@@ -242,71 +288,67 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         // ---------------------------------------------------------------- MMAs
         const uint32_t idesc1 = tc::idesc_bf16_f32(kTok, r16, false, BWD);
         const uint32_t idesc2 = tc::idesc_bf16_f32(kTok, kStep, false, BWD);
+        // descriptors of slot 0 and of t; the start address is their lowest field, in 16 bytes
+        const uint64_t tok_desc = tc::smem_desc_sw128(smem_base, 16u, 1024u);
+        const uint64_t w1_desc = tc::smem_desc_sw128(smem_base + kTokBytes, BWD ? 8192u : 16u, 1024u);
+        const uint64_t w2_desc = tc::smem_desc_sw128(smem_base + kTokBytes, BWD ? 8192u : 16u, 1024u);
+        const uint64_t t_desc = tc::smem_desc_sw128(t_base, 16u, 1024u);
         uint32_t it = 0, tiles = 0, acc2 = 0;
         int s = 0;
         bool ok = true;
         int tile = blockIdx.x;
-        AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err), t_next;
+        AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, kNoneTok, tile, err), t_next;
         for (; ok && t.adapter >= 0; t = t_next) {
             tile += gridDim.x;
-            t_next = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
+            t_next = find_tile(a.offsets, a.n, a.M, kTok, kNoneTok, tile, err);
             if (t.adapter >= a.n) continue;
-            if (kb1 > kb0) {
-                ok = tc::mbar_wait(acc1_empty, (tiles & 1u) ^ 1u, err);
-                for (int b = kb0; b < kb1 && ok; ++b) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(full(s), (it / slots) & 1u, err));
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    if (tc::elect_one()) {
-                        const uint32_t tok = slot_at(s), w = tok + kTokBytes;
+            const bool me = tc::elect_one();
+            if (me) {
+                uint32_t jt = it, jacc = acc2;
+                int js = s;
+                if (kb1 > kb0) {
+                    ok = tc::mbar_wait(acc1_empty, (tiles & 1u) ^ 1u, err);
+                    for (int b = kb0; b < kb1 && ok; ++b, ++jt) {
+                        if (!(ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err))) break;
+                        tc::tc_fence_after();
+                        const uint32_t off = js * (ua.slot_bytes >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < kStep / 16; ++kk) {
-                            const uint64_t ad = tc::smem_desc_sw128(tok + kk * 32u, 16u, 1024u);
-                            const uint64_t bd = BWD ? tc::smem_desc_sw128(w + kk * 2048u, 8192u, 1024u)
-                                                    : tc::smem_desc_sw128(w + kk * 32u, 16u, 1024u);
-                            tc::mma_f16_ss(tmem, ad, bd, idesc1, (b > kb0 || kk > 0) ? 1u : 0u);
-                        }
-                        tc::mma_commit(free1(s));
-                        if (b + 1 == kb1) tc::mma_commit(acc1_full);
+                        for (int kk = 0; kk < kStep / 16; ++kk)
+                            tc::mma_f16_ss(tmem, tok_desc + off + kk * 2u, w1_desc + off + kk * (BWD ? 128u : 2u), idesc1,
+                                           (b > kb0 || kk > 0) ? 1u : 0u);
+                        tc::mma_commit(free1(js));
+                        if (++js == slots) js = 0;
                     }
-                    __syncwarp();
-                    ++it;
-                    if (++s == slots) s = 0;
+                    if (ok) tc::mma_commit(acc1_full);
                 }
-            }
-            if (ok && nb1 > nb0) {
-                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(t_full, tiles & 1u, err));
-                tc::fence_proxy_async_smem();  // t was written by threads
-                tc::tc_fence_after();
-                for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
-                    const int i = acc2 & 1;
-                    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc2_empty(i), ((acc2 >> 1) & 1u) ^ 1u, err) &&
-                                                     tc::mbar_wait(full(s), (it / slots) & 1u, err));
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    if (tc::elect_one()) {
-                        const uint32_t w = slot_at(s) + kTokBytes, d = tmem + kAccCol + i * kStep;
+                if (ok && nb1 > nb0) {
+                    ok = tc::mbar_wait(t_full, tiles & 1u, err);
+                    tc::fence_proxy_async_smem();  // t was written by threads
+                    for (int b = nb0; b < nb1 && ok; ++b, ++jt, ++jacc) {
+                        const uint32_t i = jacc & 1;
+                        ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err) &&
+                             tc::mbar_wait(acc2_empty(i), ((jacc >> 1) & 1u) ^ 1u, err);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        const uint32_t off = js * (ua.slot_bytes >> 4), d = tmem + kAccCol + i * kStep;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             if (kk * 16 < r16) {
-                                const uint32_t p = kk / 4, in = kk % 4;
-                                const uint64_t bd = BWD ? tc::smem_desc_sw128(w + kk * 2048u, 8192u, 1024u)
-                                                        : tc::smem_desc_sw128(w + p * 8192u + in * 32u, 16u, 1024u);
-#pragma unroll
-                                for (int part = 0; part < 2; ++part) {
-                                    const uint64_t ad = tc::smem_desc_sw128(
-                                        t_base + part * part_bytes + p * kTokBytes + in * 32u, 16u, 1024u);
-                                    tc::mma_f16_ss(d, ad, bd, idesc2, (part > 0 || kk > 0) ? 1u : 0u);
-                                }
+                                const uint64_t td = t_desc + (kk / 4) * (kTokBytes >> 4) + (kk % 4) * 2u;
+                                const uint64_t wd = w2_desc + off + (BWD ? kk * 128u : (kk / 4) * 512u + (kk % 4) * 2u);
+                                tc::mma_f16_ss(d, td, wd, idesc2, kk > 0 ? 1u : 0u);
+                                tc::mma_f16_ss(d, td + (part_bytes >> 4), wd, idesc2, 1u);
                             }
                         }
                         tc::mma_commit(acc2_full(i));
+                        if (++js == slots) js = 0;
                     }
-                    __syncwarp();
-                    ++it;
-                    if (++s == slots) s = 0;
                 }
             }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1);
+            it += (kb1 - kb0) + (nb1 - nb0);
+            acc2 += nb1 - nb0;
+            s = it % slots;
             ++tiles;
         }
         __syncwarp();
@@ -326,29 +368,36 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         int s = 0;
         bool ok = true;
         int tile = blockIdx.x;
-        AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, tile, err), t_next;
+        AdapterTile t = find_tile(a.offsets, a.n, a.M, kTok, kNoneTok, tile, err), t_next;
         if (cs > 1) cluster_wait();  // every block's barriers are set up
         // A warp whose wait gave up goes through the remaining tiles without work or waits: the others
         // meet it at the barriers below.
         for (; t.adapter >= 0; t = t_next) {
             tile += gridDim.x;
-            t_next = find_tile(a.offsets, a.n, a.M, kTok, tile, err);
+            t_next = find_tile(a.offsets, a.n, a.M, kTok, kNoneTok, tile, err);
             const int my_row = tid < t.count ? checked_row(a.rows, t.first + tid, a.M, err) : -1;
             if (t.adapter >= a.n) {
                 // rows without an adapter: t = 0, out = base (this block's columns)
                 if (a.t && q == 0 && set == 0 && my_row >= 0)
                     for (int r = 0; r < a.rank; ++r) a.t[static_cast<int64_t>(my_row) * a.rank + r] = 0.f;
                 if (a.out && a.out != a.base) {
+                    // 16 rows, pieces of 16 bytes side by side over the epilogue's threads
                     const int64_t c0 = static_cast<int64_t>(nb0) * kStep;
-                    const int64_t c1 = min(a.N, static_cast<int64_t>(nb1) * kStep);
-                    for (int m = set; m < 32; m += 2) {
-                        const int row = __shfl_sync(0xFFFFFFFFu, my_row, m);
-                        if (row < 0) continue;
-                        const uint16_t* src = a.base + static_cast<int64_t>(row) * a.N;
-                        uint16_t* dst = a.out + static_cast<int64_t>(row) * a.N;
-#pragma unroll 4
-                        for (int64_t c = c0 + lane * 8; c < c1; c += 256)
-                            *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
+                    const int pieces = static_cast<int>((min(a.N, static_cast<int64_t>(nb1) * kStep) - c0) / 8);
+                    for (int m0 = 0; m0 < t.count; m0 += 4) {
+                        int row[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            row[i] = m0 + i < t.count ? checked_row(a.rows, t.first + m0 + i, a.M, err) : -1;
+                        for (int e = eid; e < pieces; e += 32 * kEpiWarps) {
+                            uint4 v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (row[i] >= 0) v[i] = *reinterpret_cast<const uint4*>(a.base + row[i] * a.N + c0 + e * 8);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (row[i] >= 0) *reinterpret_cast<uint4*>(a.out + row[i] * a.N + c0 + e * 8) = v[i];
+                        }
                     }
                 }
                 continue;
@@ -358,16 +407,21 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const bool box = __all_sync(0xFFFFFFFFu, my_row >= 0 && my_row == row0 + lane);
             const float scale = a.scale ? a.scale[t.adapter] : 1.f;
             // ---- this block's share of t, to the rows' owners.  It is put where the owner's rows of t
-            // will arrive: t_full of the last tile said that the owners have read their inboxes and
-            // that the old t is here, the barrier below that every warp is done with it.
+            // will arrive: t_full of the last tile said that the old t is here, the barrier that every
+            // warp is done with it, and peers_ready that every block's inbox is free, which its
+            // epilogue has used for tiles of out.
             if (tiles > 0) {
                 ok = ok && tc::mbar_wait(t_full, (tiles & 1u) ^ 1u, err);
+                if (lane == 0) tc::bulk_wait_group_read<0>();
                 epilogue_sync();
+                if (eid < static_cast<int>(cs)) tc::mbar_arrive_cluster(cluster_map(peers_ready, eid));
+                __syncwarp();
+                ok = ok && tc::mbar_wait(peers_ready, (tiles & 1u) ^ 1u, err);
             }
             if (ok && kb1 > kb0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc::tc_fence_after();
-            const uint32_t owner = static_cast<uint32_t>(tid / own_rows), rl = tid % own_rows;
+            const uint32_t owner = static_cast<uint32_t>(tid >> own_shift), rl = tid & (own_rows - 1);
             for (int g = set; g < segs && ok; g += 2) {
                 uint32_t v[32];
                 if (kb1 > kb0) {
@@ -378,12 +432,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
                 const int pieces = min(8, (r16 - g * 32) / 4);
-                const uint32_t at = rl / grp * (grp * 128u);  // of the group in the segment
+                const uint32_t at = (rl >> grp_shift) * (grp * 128u);  // of the group in the segment
                 const uint32_t home = owner == q ? inbox + (q * segs + g) * seg_bytes : t_base + g * kTokBytes + owner * seg_bytes;
-                uint4* to = reinterpret_cast<uint4*>(smem_raw + (home + at - tc::smem_u32(smem_raw))) + rl % grp;
+                uint4* to = reinterpret_cast<uint4*>(smem_raw + (home + at - tc::smem_u32(smem_raw))) + (rl & (grp - 1));
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (j < pieces) to[j * grp] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    if (j < pieces) to[j << grp_shift] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 for (int o = 0; o < 32; o += grp) {
@@ -407,8 +461,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             // ---- the rows this block owns
             ok = ok && tc::mbar_wait(inbox_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            for (int e = eid; e < own_rows * (r16 / 8) && ok; e += 32 * kEpiWarps) {
-                const int rr = e % own_rows, c = e / own_rows, m = static_cast<int>(q) * own_rows + rr;
+            for (int e = eid; e < (r16 / 8) << own_shift && ok; e += 32 * kEpiWarps) {
+                const int rr = e & (own_rows - 1), c = e >> own_shift, m = static_cast<int>(q) * own_rows + rr;
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -416,9 +470,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll 4
                     for (uint32_t src = 0; src < cs; ++src) {
                         const float4* at = reinterpret_cast<const float4*>(
-                            smem_raw + (inbox + (src * segs + c / 4) * seg_bytes + rr / grp * (grp * 128u) -
-                                        tc::smem_u32(smem_raw))) + rr % grp;
-                        const float4 f0 = at[c % 4 * 2 * grp], f1 = at[(c % 4 * 2 + 1) * grp];
+                            smem_raw + (inbox + (src * segs + c / 4) * seg_bytes + (rr >> grp_shift) * (grp * 128u) -
+                                        tc::smem_u32(smem_raw))) + (rr & (grp - 1));
+                        const float4 f0 = at[(c % 4 * 2) << grp_shift], f1 = at[(c % 4 * 2 + 1) << grp_shift];
                         v[0] += f0.x;
                         v[1] += f0.y;
                         v[2] += f0.z;
@@ -463,7 +517,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             // ---- out = base + the second product
             it += kb1 - kb0;
             s = it % slots;
-            int held = -1;  // slot that this warp's TMA store may still be reading
+            uint8_t* mine = smem_raw + (staging - tc::smem_u32(smem_raw)) + (warp - 2) * 4096;
             for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
                 const int i = acc2 & 1;
                 if (i != set) {
@@ -486,39 +540,34 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 tc::tmem_wait_ld();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(acc2_empty(i));
+                if (lane == 0) {
+                    tc::mbar_arrive(acc2_empty(i));
+                    tc::mbar_arrive(free2(s));
+                    tc::bulk_wait_group_read<0>();  // this warp's last store has left the staging tile
+                }
+                __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     y[c].x = add_bf16x2(y[c].x, v[c * 8], v[c * 8 + 1]);
                     y[c].y = add_bf16x2(y[c].y, v[c * 8 + 2], v[c * 8 + 3]);
                     y[c].z = add_bf16x2(y[c].z, v[c * 8 + 4], v[c * 8 + 5]);
                     y[c].w = add_bf16x2(y[c].w, v[c * 8 + 6], v[c * 8 + 7]);
+                    *reinterpret_cast<uint4*>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = y[c];
                 }
-#pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tok + lane * 128 + ((c ^ (lane & 7)) << 4)) = y[c];
                 if (box) {
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tc::tma_store_2d(&map_out, slot_at(s) + w4 * 4096u, b * kStep, row0);
+                        tc::tma_store_2d(&map_out, staging + (warp - 2) * 4096u, b * kStep, row0);
                         tc::bulk_commit_group();
-                        if (held >= 0) {
-                            tc::bulk_wait_group_read<1>();
-                            tc::mbar_arrive(free2(held));
-                        }
-                        if (slots < 6) {  // too few to leave this one for later
-                            tc::bulk_wait_group_read<0>();
-                            tc::mbar_arrive(free2(s));
-                        }
                     }
-                    held = slots < 6 ? -1 : s;
                 } else {
                     __syncwarp();
                     // eight lanes store the 128 bytes of a row
                     const int64_t col = static_cast<int64_t>(b) * kStep + (lane & 7) * 8;
 #pragma unroll
                     for (int g = 0; g < 8; ++g)
-                        y[g] = *reinterpret_cast<const uint4*>(tok + (g * 4 + (lane >> 3)) * 128 +
+                        y[g] = *reinterpret_cast<const uint4*>(mine + (g * 4 + (lane >> 3)) * 128 +
                                                                (((lane & 7) ^ ((g * 4 + (lane >> 3)) & 7)) << 4));
 #pragma unroll
                     for (int g = 0; g < 8; ++g) {
@@ -526,18 +575,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         if (row >= 0 && col < a.N)
                             *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row) * a.N + col) = y[g];
                     }
-                    tc::fence_proxy_async_smem();  // the slot is written by a TMA load next
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(free2(s));
                 }
                 ++it;
                 if (++s == slots) s = 0;
             }
-            if (held >= 0 && lane == 0) {
-                tc::bulk_wait_group_read<0>();
-                tc::mbar_arrive(free2(held));
-            }
-            __syncwarp();
             ++tiles;
         }
         // t of the last tile has arrived and the stores have completed before the block ends
@@ -625,8 +667,8 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     ua.r16 = (a.rank + 15) / 16 * 16;
     ua.panels = (a.rank + 63) / 64;
     ua.slot_bytes = nq::kTokBytes + static_cast<uint32_t>(ua.panels) * 8192u;
-    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + (ua.r16 + 31) / 32 * static_cast<size_t>(nq::kTokBytes) +
-                         8 * (3 * nq::kMaxSlots) + 80;
+    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + nq::inbox_bytes((ua.r16 + 31) / 32) +
+                         8 * (3 * nq::kMaxSlots) + 88;
     ua.slots = static_cast<int>(std::min<size_t>(nq::kMaxSlots, (kUmmaSmemMax - fixed) / ua.slot_bytes));
     const size_t smem = fixed + ua.slots * static_cast<size_t>(ua.slot_bytes);
 
@@ -661,13 +703,17 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
                 return NQ_ERR_LAUNCH;
         attr_done[dev].store(true, std::memory_order_release);
     }
-    // The fewest tiles that M rows can make decide how many blocks share one: as many as a portable
-    // cluster has while every tile's cluster is resident at once.  Clusters loop over the tiles that
-    // a finer grouping adds.
+    // The tiles decide how many blocks share one: as many as a portable cluster has while every
+    // tile's cluster is resident at once.  How many there are depends on the lists, which only the
+    // device has: M / 128 full ones and, for every other group, one that is not.  Clusters loop
+    // over what a finer grouping adds.
     const int64_t least = (a.M + nq::kTok - 1) / nq::kTok;
+    const int64_t most = nq::max_adapter_tiles(a.M, a.n, nq::kTok, nq::kNoneTok);
+    const int64_t likely = least + std::min<int64_t>(a.n, a.M) / 2;
     int cs = 8;
-    while (cs > 1 && least > resident_clusters(dev, cs)) cs /= 2;
-    const int64_t clusters = std::min<int64_t>(nq::max_adapter_tiles(a.M, a.n, nq::kTok), resident_clusters(dev, cs));
+    ua.own_shift = 4;
+    for (; cs > 1 && likely > resident_clusters(dev, cs); cs /= 2) ++ua.own_shift;
+    const int64_t clusters = std::min<int64_t>(most, resident_clusters(dev, cs));
     void* kargs[] = {&mz, &mz32, &mz1, &mbase, &mbase32, &mbase1, &mout, &ma, &mb, &ua};
     return nq_host::launch_ex(fn, dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(cs)),
                               dim3(nq::kUmmaThreads), smem, stream, kargs, pdl, cs) == cudaSuccess
