@@ -23,7 +23,18 @@ struct AdapterArgs {
     int64_t M;
     int n, rank;
     unsigned int* err;
+    // For the sums over tokens on the tensor cores: u, and t_in [M][rank] fp32, as the sum of two bf16
+    // values, rows in the order of `rows` with every adapter's padded to a multiple of 16 by zeros:
+    // part p of padded row i at parts + (p part_rows + i) part_ld.  nullptr: not wanted.
+    const float* t_in;
+    uint16_t* u_parts;
+    uint16_t* t_parts;
+    int64_t part_rows;
+    int part_ld;
 };
+
+// Padded rows of M rows in n groups, at most.
+inline int64_t max_padded_rows(int64_t M, int64_t n) { return M + 15 * (n < M ? n : M); }
 
 // Sum over the tokens of each adapter (a = blockIdx.y):
 //   gA_a[r][j] = sum_m u[m][r] x[m][j],   gB_a[i][r] = sum_m ybar[m][i] t[m][r]
@@ -46,6 +57,7 @@ struct AdapterTile {
     int adapter;  // n: rows without an adapter; -1: no such tile
     int first;    // index into rows
     int count;
+    int padded;   // padded row of the tile's first (of every group's rows in multiples of 16)
 };
 
 // Bounds of adapter a's entries in `rows`, forced into 0 <= first <= last <= M whatever the
@@ -67,6 +79,7 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
                                                  int none_per_tile, int tile, unsigned int* err) {
     const int lane = threadIdx.x & 31;
     int before = 0;  // tiles of the groups before this batch of 32
+    int padded = 0;  // and their rows in multiples of 16
     for (int a0 = 0; a0 <= n; a0 += 32) {
         const int a = a0 + lane;
         int first = 0, last = 0;
@@ -88,12 +101,29 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
             const int off = (local - (__shfl_sync(0xFFFFFFFFu, upto, src) - __shfl_sync(0xFFFFFFFFu, mine, src))) *
                             (t.adapter < n ? rows_per_tile : none_per_tile);
             t.first = __shfl_sync(0xFFFFFFFFu, first, src) + off;
+            t.padded = padded + static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < src ? (last - first + 15) & ~15 : 0)) +
+                       off;
             t.count = min(t.adapter < n ? rows_per_tile : none_per_tile, __shfl_sync(0xFFFFFFFFu, last, src) - t.first);
             return t;
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, (last - first + 15) & ~15));
     }
-    return {-1, 0, 0};
+    return {-1, 0, 0, 0};
+}
+
+// Adapter a's bounds in `rows` and its first padded row.  A whole warp calls it.
+__device__ __forceinline__ int find_group(const int32_t* offsets, int n, int64_t M, int adapter, int& first, int& last,
+                                          unsigned int* err) {
+    const int lane = threadIdx.x & 31;
+    int padded = 0;
+    for (int a0 = 0; a0 < adapter; a0 += 32) {
+        int f = 0, l = 0;
+        if (a0 + lane < adapter) adapter_bounds(offsets, n, M, a0 + lane, f, l, err);
+        padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, (l - f + 15) & ~15));
+    }
+    adapter_bounds(offsets, n, M, adapter, first, last, err);
+    return padded;
 }
 
 // Upper bound of the number of tiles for any grouping of M rows into n adapters and "none"

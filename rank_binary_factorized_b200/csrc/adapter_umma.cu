@@ -22,8 +22,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "adapter.cuh"
-#include "tc_common.cuh"
+#include "adapter_tc.cuh"
 
 namespace nq {
 
@@ -46,26 +45,10 @@ struct AdapterUmmaArgs {
     int own_shift; // log2(128 / blocks of the cluster)
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
-}
-
 // Two bf16 values and two fp32 addends, rounded once.
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t y, uint32_t lo, uint32_t hi) {
     return pack_bf16(__uint_as_float(y << 16) + __uint_as_float(lo),
                      __uint_as_float(y & 0xFFFF0000u) + __uint_as_float(hi));
-}
-
-// What v's bf16 part leaves of it (nothing of an infinity).
-__device__ __forceinline__ float rest_of(float v, uint32_t part) {
-    const float p = __uint_as_float(part);
-    return isinf(p) ? 0.f : v - p;
-}
-
-// Two fp32 values as the sum of two bf16 values each.
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(a, b);
-    lo = pack_bf16(rest_of(a, hi << 16), rest_of(b, hi & 0xFFFF0000u));
 }
 
 // Barrier of the epilogue's warps.
@@ -502,6 +485,30 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                               (((c % 8) ^ (m & 7)) << 4);
                 *reinterpret_cast<uint4*>(at) = hi;
                 *reinterpret_cast<uint4*>(at + part_bytes) = lo;
+                if constexpr (BWD) {
+                    if (m < ((t.count + 15) & ~15)) {
+                        const int64_t to = (static_cast<int64_t>(t.padded) + m) * a.part_ld + c * 8;
+                        const int64_t part = a.part_rows * a.part_ld;
+                        if (a.u_parts) {
+                            *reinterpret_cast<uint4*>(a.u_parts + to) = hi;
+                            *reinterpret_cast<uint4*>(a.u_parts + part + to) = lo;
+                        }
+                        if (a.t_parts) {
+                            const int row = m < t.count ? a.rows[t.first + m] : -1;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                v[j] = row >= 0 && row < a.M && c * 8 + j < a.rank
+                                           ? a.t_in[static_cast<int64_t>(row) * a.rank + c * 8 + j]
+                                           : 0.f;
+                            split_bf16(v[0], v[1], hi.x, lo.x);
+                            split_bf16(v[2], v[3], hi.y, lo.y);
+                            split_bf16(v[4], v[5], hi.z, lo.z);
+                            split_bf16(v[6], v[7], hi.w, lo.w);
+                            *reinterpret_cast<uint4*>(a.t_parts + to) = hi;
+                            *reinterpret_cast<uint4*>(a.t_parts + part + to) = lo;
+                        }
+                    }
+                }
             }
             tc::fence_proxy_async_smem();  // the copies and the tensor cores read t
             epilogue_sync();
@@ -607,23 +614,6 @@ namespace {
 
 constexpr size_t kUmmaSmemMax = 227 * 1024;
 
-// bf16 tensor of `dims` dimensions, innermost first, 128-byte swizzle.
-bool tmap_bf16(CUtensorMap* map, const void* base, int dims, const int64_t* extent, const int64_t* stride_elems,
-               const int* box) {
-    auto enc = nq_host::tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t d[3], st[2];
-    cuuint32_t bx[3], es[3] = {1, 1, 1};
-    for (int i = 0; i < dims; ++i) {
-        d[i] = static_cast<cuuint64_t>(extent[i]);
-        bx[i] = static_cast<cuuint32_t>(box[i]);
-        if (i > 0) st[i - 1] = static_cast<cuuint64_t>(stride_elems[i - 1]) * 2;
-    }
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(dims), const_cast<void*>(base), d, st, bx, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 namespace {
@@ -682,11 +672,11 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     const uint16_t* base = second ? a.base : a.z;
     const uint16_t* out = second ? a.out : a.z;
     const int64_t* bd = second ? base_dims : z_dims;
-    if (!tmap_bf16(&mz, a.z, 2, z_dims, &a.K, box) || !tmap_bf16(&mz32, a.z, 2, z_dims, &a.K, box32) ||
-        !tmap_bf16(&mz1, a.z, 2, z_dims, &a.K, row_box) || !tmap_bf16(&mbase, base, 2, bd, bd, box) ||
-        !tmap_bf16(&mbase32, base, 2, bd, bd, box32) || !tmap_bf16(&mbase1, base, 2, bd, bd, row_box) ||
-        !tmap_bf16(&mout, out, 2, bd, bd, box32) ||
-        !tmap_bf16(&ma, a.A, 3, a_dims, a_st, a_box) || !tmap_bf16(&mb, a.B, 3, b_dims, b_st, b_box))
+    if (!nq_host::tmap_bf16(&mz, a.z, 2, z_dims, &a.K, box) || !nq_host::tmap_bf16(&mz32, a.z, 2, z_dims, &a.K, box32) ||
+        !nq_host::tmap_bf16(&mz1, a.z, 2, z_dims, &a.K, row_box) || !nq_host::tmap_bf16(&mbase, base, 2, bd, bd, box) ||
+        !nq_host::tmap_bf16(&mbase32, base, 2, bd, bd, box32) || !nq_host::tmap_bf16(&mbase1, base, 2, bd, bd, row_box) ||
+        !nq_host::tmap_bf16(&mout, out, 2, bd, bd, box32) ||
+        !nq_host::tmap_bf16(&ma, a.A, 3, a_dims, a_st, a_box) || !nq_host::tmap_bf16(&mb, a.B, 3, b_dims, b_st, b_box))
         return NQ_ERR_LAUNCH;
 
     const void* fn = backward ? reinterpret_cast<const void*>(nq::adapter_umma_kernel<true>)

@@ -33,6 +33,8 @@ nq_status nq_launch_sign_grads(const nq_lrb_layer* L, const nq_lrb_layer* X, con
 nq_status nq_launch_adapter_rows(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl);
 bool nq_adapter_umma_fits(const nq::AdapterArgs& a);
 nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl);
+nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint16_t* u_parts, const uint16_t* t_parts,
+                                       int64_t part_rows, int part_ld, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_grad_any(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_group_rows(const int32_t* ids, int64_t M, int n, int32_t* rows, int32_t* offsets,
                                        cudaStream_t stream, bool pdl);
@@ -449,9 +451,11 @@ nq_status check_adapters(const nq_adapters* S, int64_t M) {
     return NQ_OK;
 }
 
-// Workspace: u [M][rank] fp32 of the backward pass.
+// Workspace of the backward pass: u [M][rank] fp32, or u and t in two bf16 parts each, in padded rows.
 size_t adapter_ws(const nq_adapters* S, int64_t M) {
-    return NQ_WS_HEADER_BYTES + (static_cast<size_t>(M) * S->rank * sizeof(float) + 255) / 256 * 256;
+    const size_t u = static_cast<size_t>(M) * S->rank * sizeof(float);
+    const size_t parts = 8 * static_cast<size_t>(nq::max_padded_rows(M, S->n)) * ((S->rank + 63) / 64 * 64);
+    return NQ_WS_HEADER_BYTES + (std::max(u, parts) + 255) / 256 * 256;
 }
 
 nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const int32_t* offsets, int64_t M) {
@@ -472,8 +476,10 @@ nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const in
     return a;
 }
 
+bool on_tensor_cores(const nq::AdapterArgs& a) { return a.M > 16 && nq_adapter_umma_fits(a); }
+
 nq_status launch_adapter(const nq::AdapterArgs& a, bool backward, cudaStream_t stream) {
-    if (a.M > 16 && nq_adapter_umma_fits(a)) return nq_launch_adapter_umma(a, backward, stream, pdl_enabled());
+    if (on_tensor_cores(a)) return nq_launch_adapter_umma(a, backward, stream, pdl_enabled());
     return nq_launch_adapter_rows(a, backward, stream, pdl_enabled());
 }
 
@@ -526,17 +532,27 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
     DeviceInfo* d = current_device();
     if (!d || !d->ok) return NQ_ERR_DEVICE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    float* u = reinterpret_cast<float*>(static_cast<char*>(ws) + NQ_WS_HEADER_BYTES);
-    if (xbar_out || gA) {
-        nq::AdapterArgs a = adapter_args(S, rows, offsets, M);
-        a.z = ybar;
-        a.base = xbar;
-        a.out = xbar_out;
+    char* scratch = static_cast<char*>(ws) + NQ_WS_HEADER_BYTES;
+    float* u = reinterpret_cast<float*>(scratch);
+    nq::AdapterArgs a = adapter_args(S, rows, offsets, M);
+    a.z = ybar;
+    a.base = xbar;
+    a.out = xbar_out;
+    a.K = S->d_out;
+    a.N = S->d_in;
+    const bool tensor_cores = on_tensor_cores(a);
+    if (tensor_cores) {
+        a.part_rows = nq::max_padded_rows(M, S->n);
+        a.part_ld = static_cast<int>((S->rank + 63) / 64 * 64);
+        uint16_t* parts = reinterpret_cast<uint16_t*>(scratch);
+        a.t_in = t;
+        if (gA) a.u_parts = parts;
+        if (gB) a.t_parts = parts + 2 * a.part_rows * a.part_ld;
+    } else {
         a.t = gA ? u : nullptr;
-        a.K = S->d_out;
-        a.N = S->d_in;
-        if ((st = launch_adapter(a, true, s)) != NQ_OK) return st;
     }
+    if (xbar_out || gA || (tensor_cores && gB))
+        if ((st = launch_adapter(a, true, s)) != NQ_OK) return st;
     if (!gA && !gB) return NQ_OK;
     nq::AdapterGradArgs g{};
     g.rows = rows;
@@ -553,6 +569,9 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
     g.n = static_cast<int>(S->n);
     g.rank = static_cast<int>(S->rank);
     g.err = nq_host::error_word();
+    if (tensor_cores)
+        return nq_launch_adapter_wgrad_umma(g, a.u_parts ? a.u_parts : a.t_parts, a.t_parts ? a.t_parts : a.u_parts,
+                                            a.part_rows, a.part_ld, s, pdl_enabled());
     return nq_launch_adapter_grad_any(g, s, pdl_enabled());
 }
 
