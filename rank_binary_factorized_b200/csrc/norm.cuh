@@ -35,6 +35,7 @@ struct NormBwdArgs {
     int64_t M, d, ld_gate;
     float alpha, eps, w_offset;
     bool post, h_f32;
+    unsigned int* err;
 };
 
 struct NormSumArgs {
