@@ -59,84 +59,189 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* red) {
 }
 
 // ------------------------------------------------------------------ a thread's share of a row
-// E elements of a row in a block of T threads.  VEC: pieces of 8 neighbours (16 bytes of bf16), the
-// row starts on 16 bytes; else single elements, neighbouring threads side by side.
-template <bool VEC>
-__device__ __forceinline__ int col_of(int e) {
-    return VEC ? ((e / 8) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8 + e % 8
-               : e * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+// A thread holds E elements of a row in pieces of 8 neighbours: piece k starts at column
+// (k blockDim + tid) 8.  Where every row starts on 16 bytes (SHIFT false) a piece is one load; else a
+// row starts s elements after a 16-byte boundary, the same s for all its pieces, and a piece is cut
+// out of the two aligned vectors around it.  Elements past the row's end are 0.
+__device__ __forceinline__ int col_of(int k) {
+    return (k * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
 }
-__device__ __forceinline__ void unpack8(const uint4 w, float* v) {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
+}
+__device__ __forceinline__ void unpack8(const uint32_t (&a)[4], float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(a[i] << 16);
         v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
     }
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
+// Elements s .. s + 7 of 16 bf16 (s < 8).
+__device__ __forceinline__ void shift16(const uint32_t (&w)[8], uint32_t s, uint32_t (&o)[4]) {
+    uint32_t t[6], u[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) t[i] = s & 4u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) u[i] = s & 2u ? t[i + 1] : t[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __byte_perm(u[i], u[i + 1], s & 1u ? 0x5432u : 0x3210u);
 }
-// Elements past the row's end are 0.
-template <bool VEC, int E>
-__device__ __forceinline__ void load_row(const uint16_t* row, int d, float (&v)[E]) {
-    if constexpr (VEC) {
-        uint4 w[E / 8];
+// Elements s .. s + 7 of 12 fp32 (s < 4).
+__device__ __forceinline__ void shift32(const float (&w)[12], uint32_t s, float (&o)[8]) {
+    float t[10];
 #pragma unroll
-        for (int k = 0; k < E / 8; ++k)
-            w[k] = col_of<true>(8 * k) < d ? *reinterpret_cast<const uint4*>(row + col_of<true>(8 * k)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 10; ++i) t[i] = s & 2u ? w[i + 2 < 12 ? i + 2 : 11] : w[i];
 #pragma unroll
-        for (int k = 0; k < E / 8; ++k) unpack8(w[k], v + 8 * k);
+    for (int i = 0; i < 8; ++i) o[i] = s & 1u ? t[i + 1] : t[i];
+}
+// Eight elements from column c of a row of d; `end`: nothing from there on may be read.
+template <bool SHIFT>
+__device__ __forceinline__ void load8(const uint16_t* row, int c, int d, const uint16_t* end, float (&v)[8]) {
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if constexpr (!SHIFT) {
+        if (c < d) *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(row + c);
+        unpack8(o, v);
     } else {
+        const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) >> 1) & 7u;
+        const uint16_t* q = row + c - s;
+        if (c < d) {
+            if (end == nullptr || q + 16 <= end) {
+                uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(q);
+                if (s) *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(q + 8);
+                shift16(w, s, o);
+            } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = col_of<false>(e) < d ? bf16_bits_to_float(row[col_of<false>(e)]) : 0.f;
+                for (int i = 0; i < 4; ++i)
+                    o[i] = (c + 2 * i < d ? row[c + 2 * i] : 0u) | (c + 2 * i + 1 < d ? row[c + 2 * i + 1] << 16 : 0u);
+            }
+        }
+        unpack8(o, v);
+        if (c + 8 > d) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i >= d) v[i] = 0.f;
+        }
     }
 }
-template <bool VEC, int E>
-__device__ __forceinline__ void load_row(const float* row, int d, float (&v)[E]) {
-    if constexpr (VEC) {
+template <bool SHIFT>
+__device__ __forceinline__ void load8(const float* row, int c, int d, const float* end, float (&v)[8]) {
+    float w[12];
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-            const int c = col_of<true>(4 * k);
-            const float4 w = c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[4 * k] = w.x;
-            v[4 * k + 1] = w.y;
-            v[4 * k + 2] = w.z;
-            v[4 * k + 3] = w.w;
+    for (int i = 0; i < 12; ++i) w[i] = 0.f;
+    if constexpr (!SHIFT) {
+        if (c < d) {
+            *reinterpret_cast<float4*>(w) = reinterpret_cast<const float4*>(row + c)[0];
+            *reinterpret_cast<float4*>(w + 4) = reinterpret_cast<const float4*>(row + c)[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = w[i];
+    } else {
+        const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) >> 2) & 3u;
+        const float* q = row + c - s;
+        if (c < d) {
+            if (end == nullptr || q + 12 <= end) {
+                *reinterpret_cast<float4*>(w) = reinterpret_cast<const float4*>(q)[0];
+                *reinterpret_cast<float4*>(w + 4) = reinterpret_cast<const float4*>(q)[1];
+                if (s) *reinterpret_cast<float4*>(w + 8) = reinterpret_cast<const float4*>(q)[2];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 12; ++i)
+                    if (i >= static_cast<int>(s) && c + i - static_cast<int>(s) < d) w[i] = q[i];
+            }
+        }
+        shift32(w, s, v);
+        if (c + 8 > d) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i >= d) v[i] = 0.f;
+        }
+    }
+}
+// A vector of the norm (its start is on 16 bytes, its length need not be).
+__device__ __forceinline__ void load8_vector(const uint16_t* w, int c, int d, float (&v)[8]) {
+    if (c + 8 <= d) {
+        load8<false>(w, c, d, nullptr, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < d ? bf16_bits_to_float(w[c + i]) : 0.f;
+    }
+}
+// Stores a piece.  Where rows are shifted, a lane joins its neighbour's last s elements and its own
+// first into aligned vectors; at the ends of a warp and of the row single elements are left.  Every
+// lane of the warp calls it.
+template <bool SHIFT>
+__device__ __forceinline__ void store8(uint16_t* row, int c, int d, const float (&v)[8]) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack2(v[2 * i], v[2 * i + 1]);
+    if constexpr (!SHIFT) {
+        if (c < d) *reinterpret_cast<uint4*>(row + c) = make_uint4(p[0], p[1], p[2], p[3]);
+    } else {
+        const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 7, lane = threadIdx.x & 31;
+        uint32_t w[8], o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __shfl_up_sync(0xFFFFFFFFu, p[i], 1);
+            w[4 + i] = p[i];
+        }
+        if (s == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = p[i];
+        } else {
+            shift16(w, 8 - s, o);
+        }
+        if (c < d) {
+            if ((lane > 0 || s == 0) && c + 8 - s <= d) {
+                *reinterpret_cast<uint4*>(row + c - s) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < 8 - s && c + i < d) row[c + i] = static_cast<uint16_t>(p[i / 2] >> (i % 2 * 16));
+            }
+            if (lane == 31 || c + 16 - s > d) {  // no neighbour takes the last s
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i >= 8 - s && c + i < d) row[c + i] = static_cast<uint16_t>(p[i / 2] >> (i % 2 * 16));
+            }
+        }
+    }
+}
+template <bool SHIFT>
+__device__ __forceinline__ void store8(float* row, int c, int d, const float (&v)[8]) {
+    if constexpr (!SHIFT) {
+        if (c < d) {
+            reinterpret_cast<float4*>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     } else {
+        const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 2) & 3, lane = threadIdx.x & 31;
+        float w[12], o[8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = col_of<false>(e) < d ? row[col_of<false>(e)] : 0.f;
-    }
-}
-template <bool VEC, int E>
-__device__ __forceinline__ void store_row(uint16_t* row, int d, const float (&v)[E]) {
-    if constexpr (VEC) {
+        for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xFFFFFFFFu, v[4 + i], 1);
 #pragma unroll
-        for (int k = 0; k < E / 8; ++k) {
-            const float* f = v + 8 * k;
-            if (col_of<true>(8 * k) < d)
-                *reinterpret_cast<uint4*>(row + col_of<true>(8 * k)) =
-                    make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+        for (int i = 0; i < 8; ++i) w[4 + i] = v[i];
+        if (s == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = v[i];
+        } else {
+            shift32(w, 4 - s, o);
         }
-    } else {
+        if (c < d) {
+            if ((lane > 0 || s == 0) && c + 8 - s <= d) {
+                reinterpret_cast<float4*>(row + c - s)[0] = make_float4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<float4*>(row + c - s)[1] = make_float4(o[4], o[5], o[6], o[7]);
+            } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (col_of<false>(e) < d) row[col_of<false>(e)] = float_to_bf16_bits(v[e]);
-    }
-}
-template <bool VEC, int E>
-__device__ __forceinline__ void store_row(float* row, int d, const float (&v)[E]) {
-    if constexpr (VEC) {
+                for (int i = 0; i < 8; ++i)
+                    if (i < 8 - s && c + i < d) row[c + i] = v[i];
+            }
+            if (lane == 31 || c + 16 - s > d) {
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k)
-            if (col_of<true>(4 * k) < d)
-                *reinterpret_cast<float4*>(row + col_of<true>(4 * k)) =
-                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (col_of<false>(e) < d) row[col_of<false>(e)] = v[e];
+                for (int i = 0; i < 8; ++i)
+                    if (i >= 8 - s && c + i < d) row[c + i] = v[i];
+            }
+        }
     }
 }
 
@@ -154,51 +259,62 @@ __device__ __forceinline__ float block_sum1(float v, float* red) {
     return v;
 }
 
-// One block per row, which stays in registers: every element is read once and written once.
-// Bound by HBM; 32 elements a thread keep 100 KB and more of loads in flight per multiprocessor.
-template <bool VEC, int E, bool F32>
-__global__ void __launch_bounds__(1024 * 8 / (E > 8 ? E : 8)) block_norm_rows_kernel(const NormFwdArgs a) {
+// Few rows: one block per row, 8 elements a thread, so that a row's loads are all in flight at once and
+// what is left is the latency of one load, two reductions and the stores.
+template <bool SHIFT, bool F32>
+__global__ void __launch_bounds__(1024) block_norm_rows_kernel(const NormFwdArgs a) {
     using H = std::conditional_t<F32, float, uint16_t>;
     __shared__ float red[2][32];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t m = blockIdx.x, base = m * a.d;
-    const int d = static_cast<int>(a.d);
-    float h[E];
-    load_row<VEC, E>(static_cast<const H*>(a.h) + base, d, h);
+    const int d = static_cast<int>(a.d), c = col_of(0);
+    const int64_t all = static_cast<int64_t>(gridDim.x) * a.d;
+    float h[8], w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (a.w_pre) {
+        load8_vector(a.w_pre, c, d, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] += a.w_offset;
+    }
+    load8<SHIFT>(static_cast<const H*>(a.h) + base, c, d, static_cast<const H*>(a.h) + all, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] *= a.alpha;
     if (a.y) {
-        float y[E], f[E];
-        load_row<VEC, E>(a.y + base, d, y);
+        float y[8], g[8], wp[8];
+        load8<SHIFT>(a.y + base, c, d, a.y + all, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = wp[i] = 1.f;
+        if (a.gate && a.ld_gate > 0)
+            load8<SHIFT>(a.gate + m * a.ld_gate, c, d, a.gate + (gridDim.x - 1) * a.ld_gate + d, g);
+        else if (a.gate)
+            load8_vector(a.gate, c, d, g);
         if (a.post) {
+            if (a.w_post) {
+                load8_vector(a.w_post, c, d, wp);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wp[i] += a.w_offset;
+            }
             float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) s = fmaf(y[e], y[e], s);
+            for (int i = 0; i < 8; ++i) s = fmaf(y[i], y[i], s);
             const float rp = rsqrtf(block_sum1(s, red[0]) / static_cast<float>(d) + a.eps);
-            if (a.w_post) load_row<VEC, E>(a.w_post, d, f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) y[e] *= a.w_post ? rp * (a.w_offset + f[e]) : rp;
-        }
-        if (a.gate) {
-            load_row<VEC, E>(a.gate + m * a.ld_gate, d, f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) y[e] *= f[e];
+            for (int i = 0; i < 8; ++i) y[i] *= rp * wp[i];
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = fmaf(a.alpha, h[e], y[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) h[e] *= a.alpha;
+        for (int i = 0; i < 8; ++i) h[i] = fmaf(y[i], g[i], h[i]);
     }
-    if (a.h_out) store_row<VEC, E>(static_cast<H*>(a.h_out) + base, d, h);
+    if (a.h_out) store8<SHIFT>(static_cast<H*>(a.h_out) + base, c, d, h);
     if (a.x) {
-        float s = 0.f, f[E];
+        float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(h[e], h[e], s);
-        if (a.w_pre) load_row<VEC, E>(a.w_pre, d, f);
+        for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
         const float r = rsqrtf(block_sum1(s, red[1]) / static_cast<float>(d) + a.eps);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] *= a.w_pre ? r * (a.w_offset + f[e]) : r;
-        store_row<VEC, E>(a.x + base, d, h);
+        for (int i = 0; i < 8; ++i) h[i] *= r * w[i];
+        store8<SHIFT>(a.x + base, c, d, h);
     }
 }
 
@@ -311,22 +427,19 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_grad_any_kernel(const
     }
 }
 
-// ------------------------------------------------------------------ backward, rows in shared memory
+// ------------------------------------------------------------------ rows in shared memory
 //
-// The vectors' gradients are sums over the rows, so a block takes rows in turn and its threads keep
-// their columns' sums in registers (kGradE columns a thread).  Rows come in by bulk copies, a ring
-// ahead of the arithmetic.  All that a row's gradients need of the whole row are six sums: with
-// v = w_pre gx, r = 1 / q(h'), rp = 1 / q(y) and b = w_post gate y,
-//   sum h'^2, sum v h', sum y^2, sum b gh', sum b v, sum b h'
-// give c = mean(v h'^) / q(h') and, as dh' = gh' + r v - r h' c, also
-//   sum w_post dz y = sum b gh' + r sum b v - r c sum b h',
-// so that one block-wide reduction a row is enough.
-constexpr int kGradE = 16;
+// Many rows: a block takes rows in turn; bulk copies bring them in, a ring of stages ahead of the
+// arithmetic, and a thread has 16 columns, whose weights stay in its registers.
+constexpr int kRingE = 16;
 
-struct NormBwdSmem {
-    int stages;
+// What a stage holds of a row, and where: bf16 tensors (y, gx, the gates) and tensors of h's type.
+struct NormRing {
+    const uint16_t* s16[3];
+    const void* sh[2];
+    uint32_t off16[3], offh[2];
     uint32_t stage_bytes;
-    uint32_t off_gx, off_h, off_gh, off_gate;  // in a stage; y is first
+    int stages;
 };
 
 // Bytes [from, from + bytes) of `src`, whose `total` bytes start on 16 and whose end need not: the
@@ -340,223 +453,393 @@ __device__ __forceinline__ uint32_t span_bytes(int64_t from, uint32_t bytes, int
     return static_cast<uint32_t>(e1 > a0 ? e1 - a0 : 0);
 }
 
-template <bool VEC, bool F32>
-__global__ void __launch_bounds__(512, 1) block_norm_grad_rows_kernel(const NormBwdArgs a, const NormBwdSmem sm) {
+// Two fp32 values in one register pair.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo_of(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.v)); }
+__device__ __forceinline__ float hi_of(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.v >> 32)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// Row m into stage s, by one thread.
+template <typename H>
+__device__ __forceinline__ void load_stage(const NormRing& g, uint8_t* smem, int64_t m, int s, int64_t M, int64_t d,
+                                           uint32_t bar) {
+    const int64_t f16 = m * d * 2, fh = m * d * static_cast<int64_t>(sizeof(H));
+    bool odd16, oddh;
+    const uint32_t n16 = span_bytes(f16, static_cast<uint32_t>(d * 2), M * d * 2, odd16);
+    const uint32_t nh = span_bytes(fh, static_cast<uint32_t>(d * sizeof(H)), M * d * static_cast<int64_t>(sizeof(H)), oddh);
+    uint8_t* st = smem + s * g.stage_bytes;
+    uint32_t tx = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) tx += g.s16[i] ? n16 : 0u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tx += g.sh[i] ? nh : 0u;
+    if (odd16) {  // next to the tensor's end only
+        for (int i = 0; i < 3; ++i)
+            if (g.s16[i])
+                for (int64_t b = max((f16 + d * 2) & ~int64_t{15}, f16); b < f16 + d * 2; b += 2)
+                    *reinterpret_cast<uint16_t*>(st + g.off16[i] + (b - (f16 & ~int64_t{15}))) = g.s16[i][b / 2];
+    }
+    if (oddh) {
+        const int64_t e = fh + d * static_cast<int64_t>(sizeof(H));
+        for (int i = 0; i < 2; ++i)
+            if (g.sh[i])
+                for (int64_t b = max(e & ~int64_t{15}, fh); b < e; b += sizeof(H))
+                    *reinterpret_cast<H*>(st + g.offh[i] + (b - (fh & ~int64_t{15}))) =
+                        static_cast<const H*>(g.sh[i])[b / static_cast<int64_t>(sizeof(H))];
+    }
+    tc::mbar_arrive_expect_tx(bar, tx);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (g.s16[i] && n16)
+            tc::bulk_load(tc::smem_u32(st + g.off16[i]), reinterpret_cast<const uint8_t*>(g.s16[i]) + (f16 & ~int64_t{15}),
+                          n16, bar);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (g.sh[i] && nh)
+            tc::bulk_load(tc::smem_u32(st + g.offh[i]), static_cast<const uint8_t*>(g.sh[i]) + (fh & ~int64_t{15}), nh, bar);
+}
+
+// 1, or offset + w, of the piece at column c.
+__device__ __forceinline__ void weight8(const uint16_t* w, float offset, int c, int d, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.f;
+    if (w) {
+        load8_vector(w, c, d, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += offset;
+    }
+}
+
+// Sum over the block (up to 16 warps), in every thread, with one barrier.  `red` may be reused once
+// another barrier has passed.
+__device__ __forceinline__ float ring_sum(float v, float* red) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (lane & 15) < nw ? red[lane & 15] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void ring_get(const uint8_t* at, bool there, int c, int d, F2 (&v)[4]) {
+    float f[8];
+    load8<SHIFT>(reinterpret_cast<const T*>(at), c, there ? d : 0, static_cast<const T*>(nullptr), f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+
+// Forward: two reductions a row (of y^2, then of h'^2, which may be far smaller than its two terms:
+// it is not expanded into their sums).
+template <bool SHIFT, bool F32, bool ROWGATE>
+__global__ void __launch_bounds__(512, 1) block_norm_ring_kernel(const NormFwdArgs a, const NormRing ring, int64_t M) {
     using H = std::conditional_t<F32, float, uint16_t>;
-    constexpr int E = kGradE;
+    constexpr int P = kRingE / 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[2][6][16];
+    __shared__ float red[2][16];
     __shared__ __align__(8) uint64_t bar[4];
-    const int d = static_cast<int>(a.d), warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const int d = static_cast<int>(a.d);
     const uint32_t bar0 = tc::smem_u32(bar);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < sm.stages; ++s) tc::mbar_init(bar0 + 8u * s, 1);
+        for (int s = 0; s < ring.stages; ++s) tc::mbar_init(bar0 + 8u * s, 1);
         tc::mbar_fence_init();
     }
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    const bool row_gate = a.gate && a.ld_gate > 0;
-    const uint16_t* src16[3] = {a.y, a.gx, row_gate ? a.gate : nullptr};
-    const uint32_t off16[3] = {0u, sm.off_gx, sm.off_gate};
-    const void* srch[2] = {a.h_out, a.gh_out};
-    const uint32_t offh[2] = {sm.off_h, sm.off_gh};
-    const int64_t total16 = a.M * a.d * 2, totalh = a.M * a.d * static_cast<int64_t>(sizeof(H));
-
-    auto load = [&](int64_t m, int s) {  // one thread
-        const int64_t f16 = m * a.d * 2, fh = m * a.d * static_cast<int64_t>(sizeof(H));
-        bool odd16, oddh;
-        const uint32_t n16 = span_bytes(f16, d * 2u, total16, odd16), nh = span_bytes(fh, d * sizeof(H), totalh, oddh);
-        uint8_t* st = smem + s * sm.stage_bytes;
-        uint32_t tx = 0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) tx += src16[i] ? n16 : 0u;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) tx += srch[i] ? nh : 0u;
-        if (odd16) {  // next to the tensor's end only
-            for (int i = 0; i < 3; ++i)
-                if (src16[i])
-                    for (int64_t b = std::max((f16 + d * 2) & ~int64_t{15}, f16); b < f16 + d * 2; b += 2)
-                        *reinterpret_cast<uint16_t*>(st + off16[i] + (b - (f16 & ~int64_t{15}))) = src16[i][b / 2];
-        }
-        if (oddh) {
-            for (int i = 0; i < 2; ++i)
-                if (srch[i])
-                    for (int64_t b = std::max((fh + d * static_cast<int64_t>(sizeof(H))) & ~int64_t{15}, fh);
-                         b < fh + d * static_cast<int64_t>(sizeof(H)); b += sizeof(H))
-                        *reinterpret_cast<H*>(st + offh[i] + (b - (fh & ~int64_t{15}))) =
-                            static_cast<const H*>(srch[i])[b / static_cast<int64_t>(sizeof(H))];
-        }
-        tc::mbar_arrive_expect_tx(bar0 + 8u * s, tx);
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (src16[i] && n16)
-                tc::bulk_load(tc::smem_u32(st + off16[i]),
-                              reinterpret_cast<const uint8_t*>(src16[i]) + (f16 & ~int64_t{15}), n16, bar0 + 8u * s);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (srch[i] && nh)
-                tc::bulk_load(tc::smem_u32(st + offh[i]), static_cast<const uint8_t*>(srch[i]) + (fh & ~int64_t{15}), nh,
-                              bar0 + 8u * s);
-    };
     if (threadIdx.x == 0)
-        for (int s = 0; s < sm.stages; ++s)
-            if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < a.M) load(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+        for (int s = 0; s < ring.stages; ++s)
+            if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < M)
+                load_stage<H>(ring, smem, blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s, M, d, bar0 + 8u * s);
+    // w_pre' and w_post' times a shared gate, of this thread's columns
+    F2 wpre[P][4], wb[P][4];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        float v[8], g[8];
+        weight8(a.w_pre, a.w_offset, col_of(k), d, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wpre[k][i] = f2(v[2 * i], v[2 * i + 1]);
+        weight8(a.post ? a.w_post : nullptr, a.w_offset, col_of(k), d, v);
+        if (!ROWGATE && a.gate) {
+            load8_vector(a.gate, col_of(k), d, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wb[k][i] = f2(v[2 * i], v[2 * i + 1]);
+    }
+    const float inv_d = 1.0f / static_cast<float>(d);
+    const F2 alpha2 = f2(a.alpha, a.alpha);
+    uint32_t it = 0;
+    int s = 0;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x, ++it) {
+        // a wait that gives up leaves stale rows behind; the error word tells
+        tc::mbar_wait(bar0 + 8u * s, (it / ring.stages) & 1u, a.err);
+        const int64_t base = m * a.d;
+        const uint8_t* st16 = smem + s * ring.stage_bytes + (SHIFT ? static_cast<uint32_t>(base * 2) & 15u : 0u);
+        const uint8_t* sth = smem + s * ring.stage_bytes + ring.offh[0] +
+                             (SHIFT ? static_cast<uint32_t>(base * static_cast<int64_t>(sizeof(H))) & 15u : 0u);
+        F2 h[P][4], rp2 = f2(1.f, 1.f);
+        if (a.post) {
+            F2 sum = f2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                F2 y[4];
+                ring_get<uint16_t, SHIFT>(st16, true, col_of(k), d, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum = fma2(y[i], y[i], sum);
+            }
+            const float rp = rsqrtf(ring_sum(lo_of(sum) + hi_of(sum), red[0]) * inv_d + a.eps);
+            rp2 = f2(rp, rp);
+        }
+        F2 sum = f2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            F2 y[4], g[4];
+            ring_get<H, SHIFT>(sth, true, col_of(k), d, h[k]);
+            ring_get<uint16_t, SHIFT>(st16, a.y != nullptr, col_of(k), d, y);
+            if constexpr (ROWGATE) ring_get<uint16_t, SHIFT>(st16 + ring.off16[1], true, col_of(k), d, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                F2 z = wb[k][i] * (y[i] * rp2);
+                if constexpr (ROWGATE) z = z * g[i];
+                h[k][i] = fma2(alpha2, h[k][i], z);
+                sum = fma2(h[k][i], h[k][i], sum);
+            }
+        }
+        // the barrier in here also says that every thread is done with this stage
+        const float r = rsqrtf(ring_sum(lo_of(sum) + hi_of(sum), red[1]) * inv_d + a.eps);
+        if (threadIdx.x == 0 && m + static_cast<int64_t>(ring.stages) * gridDim.x < M) {
+            tc::fence_proxy_async_smem();
+            load_stage<H>(ring, smem, m + static_cast<int64_t>(ring.stages) * gridDim.x, s, M, d, bar0 + 8u * s);
+        }
+        if (!a.post) __syncthreads();  // red[1] is read before the next row writes it
+        const F2 r2 = f2(r, r);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            float oh[8], ox[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 x = h[k][i] * (wpre[k][i] * r2);
+                oh[2 * i] = lo_of(h[k][i]);
+                oh[2 * i + 1] = hi_of(h[k][i]);
+                ox[2 * i] = lo_of(x);
+                ox[2 * i + 1] = hi_of(x);
+            }
+            if (a.h_out) store8<SHIFT>(static_cast<H*>(a.h_out) + base, col_of(k), d, oh);
+            if (a.x) store8<SHIFT>(a.x + base, col_of(k), d, ox);
+        }
+        if (++s == ring.stages) s = 0;
+    }
+}
 
-    // the vectors, two bf16 to a register
-    uint32_t wpre[E / 2], wpost[E / 2], gt[E / 2];
-    auto load_vector = [&](const uint16_t* w, uint32_t (&out)[E / 2]) {
-        float f[E];
-        if (w) load_row<VEC, E>(w, d, f);
+// Backward: the vectors' gradients are sums over the rows, so a thread keeps its columns' sums in
+// registers.  All that a row's gradients need of the whole row are six sums: with
+// v = w_pre gx, r = 1 / q(h'), rp = 1 / q(y) and b = w_post gate y,
+//   sum h'^2, sum v h', sum y^2, sum b gh', sum b v, sum b h'
+// give c = mean(v h'^) / q(h') and, as dh' = gh' + r v - r h' c, also
+//   sum w_post dz y = sum b gh' + r sum b v - r c sum b h',
+// so that one block-wide reduction a row is enough.  With a shared gate, g_w_post and g_gate are both
+// multiples of sum_m dh' y^, column by column, so two sums a column serve three vectors.  At 8192
+// channels a multiprocessor has some 4300 cycles a row at HBM's rate, and the arithmetic alone needs
+// over half of them: it is done on pairs (two fp32 operations an instruction).
+template <bool SHIFT, bool F32, bool ROWGATE>
+__global__ void __launch_bounds__(512, 1) block_norm_grad_rows_kernel(const NormBwdArgs a, const NormRing ring) {
+    using H = std::conditional_t<F32, float, uint16_t>;
+    constexpr int P = kRingE / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[2][16][8];
+    __shared__ __align__(8) uint64_t bar[4];
+    const int d = static_cast<int>(a.d), warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const uint32_t bar0 = tc::smem_u32(bar);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ring.stages; ++s) tc::mbar_init(bar0 + 8u * s, 1);
+        tc::mbar_fence_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    if (threadIdx.x == 0)
+        for (int s = 0; s < ring.stages; ++s)
+            if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < a.M)
+                load_stage<H>(ring, smem, blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s, a.M, d, bar0 + 8u * s);
+
+    // w_pre' and w_post' times a shared gate, of this thread's columns
+    F2 wpre[P][4], wb[P][4], acc0[P][4], acc1[P][4];
 #pragma unroll
-        for (int e = 0; e < E; e += 2)  // bf16 values: exact
-            out[e / 2] = w ? (__float_as_uint(f[e]) >> 16) | (__float_as_uint(f[e + 1]) & 0xFFFF0000u) : 0x3F803F80u;
-    };
-    load_vector(a.w_pre, wpre);
-    load_vector(a.post ? a.w_post : nullptr, wpost);
-    load_vector(row_gate ? nullptr : a.gate, gt);
-    const float off_pre = a.w_pre ? a.w_offset : 0.f, off_post = a.post && a.w_post ? a.w_offset : 0.f;
-    auto half = [](const uint32_t (&w)[E / 2], int e) {
-        return __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-    };
-    float acc[3][E];
+    for (int k = 0; k < P; ++k) {
+        float v[8], g[8];
+        weight8(a.w_pre, a.w_offset, col_of(k), d, v);
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+        for (int i = 0; i < 4; ++i) wpre[k][i] = f2(v[2 * i], v[2 * i + 1]);
+        weight8(a.post ? a.w_post : nullptr, a.w_offset, col_of(k), d, v);
+        if (!ROWGATE && a.gate) {
+            load8_vector(a.gate, col_of(k), d, g);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+            for (int i = 0; i < 8; ++i) v[i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wb[k][i] = f2(v[2 * i], v[2 * i + 1]);
+            acc0[k][i] = acc1[k][i] = f2(0.f, 0.f);
+        }
+    }
     const float inv_d = 1.0f / static_cast<float>(d);
 
     uint32_t it = 0;
     int s = 0;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, ++it) {
         // a wait that gives up leaves stale rows behind; the error word tells
-        tc::mbar_wait(bar0 + 8u * s, (it / sm.stages) & 1u, a.err);
-        const uint8_t* st = smem + s * sm.stage_bytes;
+        tc::mbar_wait(bar0 + 8u * s, (it / ring.stages) & 1u, a.err);
+        const uint8_t* st = smem + s * ring.stage_bytes;
         const int64_t base = m * a.d;
-        const uint32_t lead16 = static_cast<uint32_t>(base * 2) & 15u;
-        const uint32_t leadh = static_cast<uint32_t>(base * static_cast<int64_t>(sizeof(H))) & 15u;
-        // 8 elements from a piece's first e (VEC) or one (else)
-        constexpr int P = VEC ? 8 : 1;
-        auto get16 = [&](uint32_t off, bool there, int e, float (&v)[P]) {
-            const int c = col_of<VEC>(e);
-            const bool in = there && c < d;
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(st + off + (VEC ? 0u : lead16)) + c;
-            if constexpr (VEC)
-                unpack8(in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0), v);
-            else
-                v[0] = in ? bf16_bits_to_float(*p) : 0.f;
-        };
-        auto geth = [&](uint32_t off, bool there, int e, float (&v)[P]) {
-            const int c = col_of<VEC>(e);
-            const bool in = there && c < d;
-            const H* p = reinterpret_cast<const H*>(st + off + (VEC ? 0u : leadh)) + c;
-            if constexpr (VEC && F32) {
-                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float4 f0 = in ? reinterpret_cast<const float4*>(p)[0] : z, f1 = in ? reinterpret_cast<const float4*>(p)[1] : z;
-                v[0] = f0.x, v[1] = f0.y, v[2] = f0.z, v[3] = f0.w, v[4] = f1.x, v[5] = f1.y, v[6] = f1.z, v[7] = f1.w;
-            } else if constexpr (VEC) {
-                unpack8(in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0), v);
-            } else if constexpr (F32) {
-                v[0] = in ? *p : 0.f;
-            } else {
-                v[0] = in ? bf16_bits_to_float(*p) : 0.f;
-            }
-        };
-        float sum[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const uint32_t lead16 = SHIFT ? static_cast<uint32_t>(base * 2) & 15u : 0u;
+        const uint32_t leadh = SHIFT ? static_cast<uint32_t>(base * static_cast<int64_t>(sizeof(H))) & 15u : 0u;
+        const uint8_t *py = st + lead16, *pgx = py + ring.off16[1], *pgate = py + ring.off16[2];
+        const uint8_t *ph = st + ring.offh[0] + leadh, *pgh = st + ring.offh[1] + leadh;
+        F2 part[6];
 #pragma unroll
-        for (int e0 = 0; e0 < E; e0 += P) {
-            float y[P], gx[P], h[P], gh[P], gr[P];
-            get16(0u, a.y != nullptr, e0, y);
-            get16(sm.off_gx, a.gx != nullptr, e0, gx);
-            geth(sm.off_h, true, e0, h);
-            geth(sm.off_gh, a.gh_out != nullptr, e0, gh);
-            if (row_gate) get16(sm.off_gate, true, e0, gr);
+        for (int k = 0; k < 6; ++k) part[k] = f2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float v = (off_pre + half(wpre, e0 + i)) * gx[i];
-                const float b = (off_post + half(wpost, e0 + i)) * (row_gate ? gr[i] : half(gt, e0 + i)) * y[i];
-                sum[0] = fmaf(h[i], h[i], sum[0]);
-                sum[1] = fmaf(v, h[i], sum[1]);
-                sum[2] = fmaf(y[i], y[i], sum[2]);
-                sum[3] = fmaf(b, gh[i], sum[3]);
-                sum[4] = fmaf(b, v, sum[4]);
-                sum[5] = fmaf(b, h[i], sum[5]);
+        for (int k = 0; k < P; ++k) {
+            F2 y[4], gx[4], h[4], gh[4], gr[4];
+            ring_get<uint16_t, SHIFT>(py, a.y != nullptr, col_of(k), d, y);
+            ring_get<uint16_t, SHIFT>(pgx, a.gx != nullptr, col_of(k), d, gx);
+            ring_get<H, SHIFT>(ph, true, col_of(k), d, h);
+            ring_get<H, SHIFT>(pgh, a.gh_out != nullptr, col_of(k), d, gh);
+            if constexpr (ROWGATE) ring_get<uint16_t, SHIFT>(pgate, true, col_of(k), d, gr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 v = wpre[k][i] * gx[i];
+                F2 b = wb[k][i] * y[i];
+                if constexpr (ROWGATE) b = b * gr[i];
+                part[0] = fma2(h[i], h[i], part[0]);
+                part[1] = fma2(v, h[i], part[1]);
+                part[2] = fma2(y[i], y[i], part[2]);
+                part[3] = fma2(b, gh[i], part[3]);
+                part[4] = fma2(b, v, part[4]);
+                part[5] = fma2(b, h[i], part[5]);
             }
         }
+        // 8 values over 32 lanes, halving the values a lane keeps: lane l ends with value l / 4
+        float sum[8];
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
+        for (int k = 0; k < 6; ++k) sum[k] = lo_of(part[k]) + hi_of(part[k]);
+        sum[6] = sum[7] = 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
-            if (lane == 0) red[it & 1][k][warp] = sum[k];
+        for (int w = 4; w >= 1; w /= 2) {
+            const bool upper = lane & (4 * w);
+#pragma unroll
+            for (int k = 0; k < w; ++k) {
+                const float keep = upper ? sum[k + w] : sum[k], give = upper ? sum[k] : sum[k + w];
+                sum[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4 * w);
+            }
         }
+        sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], 2);
+        sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], 1);
+        if ((lane & 3) == 0) red[it & 1][warp][lane >> 2] = sum[0];
         __syncthreads();  // and every thread is done with the last row
         if (threadIdx.x == 0 && it > 0) {
-            const int64_t ahead = m + static_cast<int64_t>(sm.stages - 1) * gridDim.x;
-            const int ps = s == 0 ? sm.stages - 1 : s - 1;
+            const int64_t ahead = m + static_cast<int64_t>(ring.stages - 1) * gridDim.x;
+            const int ps = s == 0 ? ring.stages - 1 : s - 1;
             if (ahead < a.M) {
                 tc::fence_proxy_async_smem();
-                load(ahead, ps);
+                load_stage<H>(ring, smem, ahead, ps, a.M, d, bar0 + 8u * ps);
             }
         }
+        float all = 0.f;
+        for (int w = lane & 3; w < nw; w += 4) all += red[it & 1][w][lane >> 2];
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, 1);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, 2);
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
-            sum[k] = 0.f;
-            for (int w = 0; w < nw; ++w) sum[k] += red[it & 1][k][w];
-        }
+        for (int k = 0; k < 6; ++k) sum[k] = __shfl_sync(0xFFFFFFFFu, all, 4 * k);
         const float r = rsqrtf(sum[0] * inv_d + a.eps);
         const float c = sum[1] * inv_d * r * r;  // mean(v h'^) / q(h')
         const float rp = a.post ? rsqrtf(sum[2] * inv_d + a.eps) : 1.f;
-        const float cp = (sum[3] + r * sum[4] - r * c * sum[5]) * inv_d * rp;  // mean(w_post dz y^)
+        const float cp = a.post ? (sum[3] + r * sum[4] - r * c * sum[5]) * inv_d * rp : 0.f;  // mean(w_post dz y^)
+        const F2 r2 = f2(r, r), nc2 = f2(-c, -c), rp2 = f2(rp, rp), ncp2 = f2(-cp, -cp), alpha2 = f2(a.alpha, a.alpha);
 #pragma unroll
-        for (int e0 = 0; e0 < E; e0 += P) {
-            float y[P], gx[P], h[P], gh[P], gr[P], gy[P], gg[P];
-            get16(0u, a.y != nullptr, e0, y);
-            get16(sm.off_gx, a.gx != nullptr, e0, gx);
-            geth(sm.off_h, true, e0, h);
-            geth(sm.off_gh, a.gh_out != nullptr, e0, gh);
-            if (row_gate) get16(sm.off_gate, true, e0, gr);
+        for (int k = 0; k < P; ++k) {
+            F2 y[4], gx[4], h[4], gh[4], gr[4];
+            ring_get<uint16_t, SHIFT>(py, a.y != nullptr, col_of(k), d, y);
+            ring_get<uint16_t, SHIFT>(pgx, a.gx != nullptr, col_of(k), d, gx);
+            ring_get<H, SHIFT>(ph, true, col_of(k), d, h);
+            ring_get<H, SHIFT>(pgh, a.gh_out != nullptr, col_of(k), d, gh);
+            if constexpr (ROWGATE) ring_get<uint16_t, SHIFT>(pgate, true, col_of(k), d, gr);
+            float o_y[8], o_h[8], o_g[8];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float hn = h[i] * r, gate = row_gate ? gr[i] : half(gt, e0 + i);
-                const float w = off_post + half(wpost, e0 + i);
-                const float dh = gh[i] + r * ((off_pre + half(wpre, e0 + i)) * gx[i]) - hn * c;
-                acc[0][e0 + i] = fmaf(gx[i], hn, acc[0][e0 + i]);
-                const float yn = y[i] * rp, dz = dh * gate, z = yn * w;
-                acc[1][e0 + i] = fmaf(dz, yn, acc[1][e0 + i]);
-                gg[i] = dh * z;
-                acc[2][e0 + i] += gg[i];
-                gy[i] = a.post ? rp * (w * dz - yn * cp) : dz;
-                gh[i] = a.alpha * dh;
-            }
-            const int col = col_of<VEC>(e0);
-            if (col < d) {
-                if constexpr (VEC) {
-                    auto pack = [](const float (&f)[P]) {
-                        return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-                    };
-                    if (a.gy) *reinterpret_cast<uint4*>(a.gy + base + col) = pack(gy);
-                    if (row_gate && a.g_gate_rows) *reinterpret_cast<uint4*>(a.g_gate_rows + base + col) = pack(gg);
-                    if constexpr (F32) {
-                        if (a.gh) {
-                            float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.gh) + base + col);
-                            to[0] = make_float4(gh[0], gh[1], gh[2], gh[3]);
-                            to[1] = make_float4(gh[4], gh[5], gh[6], gh[7]);
-                        }
-                    } else if (a.gh) {
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.gh) + base + col) = pack(gh);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const F2 hn = h[i] * r2;
+                const F2 dh = fma2(hn, nc2, fma2(wpre[k][i] * gx[i], r2, gh[i]));
+                acc0[k][i] = fma2(gx[i], hn, acc0[k][i]);
+                const F2 yn = y[i] * rp2;
+                F2 b = wb[k][i];
+                if constexpr (ROWGATE) {
+                    const F2 g = dh * wb[k][i] * yn;  // dh' z
+                    o_g[2 * i] = lo_of(g);
+                    o_g[2 * i + 1] = hi_of(g);
+                    b = b * gr[i];
+                    acc1[k][i] = fma2(dh * gr[i], yn, acc1[k][i]);
                 } else {
-                    if (a.gy) a.gy[base + col] = float_to_bf16_bits(gy[0]);
-                    if (row_gate && a.g_gate_rows) a.g_gate_rows[base + col] = float_to_bf16_bits(gg[0]);
-                    if (a.gh) st_h(a.gh, base + col, F32, gh[0]);
+                    acc1[k][i] = fma2(dh, yn, acc1[k][i]);
                 }
+                const F2 gy = fma2(yn, ncp2, b * dh) * rp2, g = dh * alpha2;
+                o_y[2 * i] = lo_of(gy);
+                o_y[2 * i + 1] = hi_of(gy);
+                o_h[2 * i] = lo_of(g);
+                o_h[2 * i + 1] = hi_of(g);
             }
+            if (a.gy) store8<SHIFT>(a.gy + base, col_of(k), d, o_y);
+            if (a.gh) store8<SHIFT>(static_cast<H*>(a.gh) + base, col_of(k), d, o_h);
+            if constexpr (ROWGATE)
+                if (a.g_gate_rows) store8<SHIFT>(a.g_gate_rows + base, col_of(k), d, o_g);
         }
-        if (++s == sm.stages) s = 0;
+        if (++s == ring.stages) s = 0;
     }
+    // g_w_pre; g_w_post = gate sum dh' y^; g_gate = w_post' sum dh' y^
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-        if (a.part[k]) store_row<VEC, E>(a.part[k] + static_cast<int64_t>(blockIdx.x) * a.d, d, acc[k]);
+    for (int k = 0; k < P; ++k) {
+        const int c = col_of(k);
+        float g[8], w[8], v0[8], v1[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v0[2 * i] = lo_of(acc0[k][i]);
+            v0[2 * i + 1] = hi_of(acc0[k][i]);
+            v1[2 * i] = lo_of(acc1[k][i]);
+            v1[2 * i + 1] = hi_of(acc1[k][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = 1.f;
+        if (!ROWGATE && a.gate) load8_vector(a.gate, c, d, g);
+        weight8(a.post ? a.w_post : nullptr, a.w_offset, c, d, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c + i >= d) continue;
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * a.d + c + i;
+            if (a.part[0]) a.part[0][at] = v0[i];
+            if (a.part[1]) a.part[1][at] = g[i] * v1[i];
+            if (a.part[2]) a.part[2][at] = w[i] * v1[i];
+        }
+    }
 }
 
 // out[k][i] = sum over the blocks' partial sums, in fp64: 8 threads a column, each with every eighth
@@ -585,46 +868,109 @@ __global__ void __launch_bounds__(256) norm_vector_sums_kernel(const NormSumArgs
 
 namespace {
 
-constexpr size_t kNormSmemMax = 226 * 1024;
+constexpr size_t kNormSmemMax = 227 * 1024 - 1152;  // and the static part
 
 // Threads for a row of d channels at E elements each.
 int row_threads(int64_t d, int E) { return static_cast<int>((d + 32 * E - 1) / (32 * E) * 32); }
 
-// Backward: blocks that share the rows.  Rows of up to 8192 channels take 512 threads a
-// multiprocessor with 128 registers each (16 columns' sums); wider ones two blocks of any size.
+constexpr int64_t kRingMaxD = 512 * nq::kRingE;
+
+// Blocks a multiprocessor of the ring kernels: 512 threads with 128 registers each in all.
+int ring_blocks_per_sm(int64_t d) { return std::max(1, std::min(16, 512 / row_threads(d, nq::kRingE))); }
+
+// Backward: blocks that share the rows; rows too wide for the ring take two blocks of any size.
 int grad_blocks(int64_t d, int64_t M) {
-    const int per_sm = d <= 512 * nq::kGradE ? std::max(1, std::min(16, 512 / row_threads(d, nq::kGradE))) : 2;
+    const int per_sm = d <= kRingMaxD ? ring_blocks_per_sm(d) : 2;
     return static_cast<int>(std::min<int64_t>(M, static_cast<int64_t>(per_sm) * nq_host::sm_count()));
 }
 
-template <bool VEC, bool F32>
-const void* rows_kernel(int E) {
-    return E == 8    ? reinterpret_cast<const void*>(nq::block_norm_rows_kernel<VEC, 8, F32>)
-           : E == 16 ? reinterpret_cast<const void*>(nq::block_norm_rows_kernel<VEC, 16, F32>)
-                     : reinterpret_cast<const void*>(nq::block_norm_rows_kernel<VEC, 32, F32>);
+// Lays out the stages: a row that does not start on 16 bytes brings up to 15 before and after it, and
+// its last piece is read to the end of a second vector.  False: two stages do not fit.
+bool plan_ring(nq::NormRing& g, int64_t d, bool h_f32) {
+    uint32_t at = 0;
+    auto place = [&](const void* p, size_t elem, uint32_t& off) {
+        off = at;
+        if (p) at += static_cast<uint32_t>((d * elem + 62 + 127) / 128 * 128);
+    };
+    for (int i = 0; i < 3; ++i) place(g.s16[i], 2, g.off16[i]);
+    for (int i = 0; i < 2; ++i) place(g.sh[i], h_f32 ? 4 : 2, g.offh[i]);
+    g.stage_bytes = at;
+    const size_t share = kNormSmemMax / ring_blocks_per_sm(d) - 2048;
+    g.stages = static_cast<int>(std::max<size_t>(2, std::min<size_t>(4, share / at)));
+    return static_cast<size_t>(g.stages) * at <= kNormSmemMax;
 }
+
+template <bool SHIFT, bool F32>
+const void* ring_kernel(bool row_gate) {
+    return row_gate ? reinterpret_cast<const void*>(nq::block_norm_ring_kernel<SHIFT, F32, true>)
+                    : reinterpret_cast<const void*>(nq::block_norm_ring_kernel<SHIFT, F32, false>);
+}
+template <bool SHIFT, bool F32>
+const void* grad_kernel(bool row_gate) {
+    return row_gate ? reinterpret_cast<const void*>(nq::block_norm_grad_rows_kernel<SHIFT, F32, true>)
+                    : reinterpret_cast<const void*>(nq::block_norm_grad_rows_kernel<SHIFT, F32, false>);
+}
+// The kernel for this alignment, residual type and gate, allowed all of the shared memory (set once per
+// device and kernel; setting an attribute twice is harmless).  nullptr: failed.
+const void* pick(bool backward, bool shift, bool f32, bool row_gate) {
+    const void* fns[2][8] = {{ring_kernel<false, false>(false), ring_kernel<false, false>(true),
+                              ring_kernel<false, true>(false), ring_kernel<false, true>(true),
+                              ring_kernel<true, false>(false), ring_kernel<true, false>(true),
+                              ring_kernel<true, true>(false), ring_kernel<true, true>(true)},
+                             {grad_kernel<false, false>(false), grad_kernel<false, false>(true),
+                              grad_kernel<false, true>(false), grad_kernel<false, true>(true),
+                              grad_kernel<true, false>(false), grad_kernel<true, false>(true),
+                              grad_kernel<true, true>(false), grad_kernel<true, true>(true)}};
+    const int i = (shift ? 4 : 0) + (f32 ? 2 : 0) + (row_gate ? 1 : 0);
+    static std::atomic<bool> done[64][2][8];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return nullptr;
+    const void* fn = fns[backward][i];
+    if (!done[dev][backward][i].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormSmemMax)) !=
+            cudaSuccess)
+            return nullptr;
+        done[dev][backward][i].store(true, std::memory_order_release);
+    }
+    return fn;
+}
+
+nq_status launched(cudaError_t e) { return e == cudaSuccess ? NQ_OK : NQ_ERR_LAUNCH; }
 
 }  // namespace
 
 nq_status nq_launch_block_norm(const nq::NormFwdArgs& a, int64_t M, cudaStream_t stream, bool pdl) {
     nq::NormFwdArgs args = a;
-    void* kargs[] = {&args};
-    // Few rows: as many threads a row as there are pieces of 8, for the latency; many: 32 elements a
-    // thread, for loads in flight at few threads.  A block has at most 8192 / E threads of E
-    // elements, so that its registers fit: rows over 8192 channels go through the other kernel.
-    int E = 8;
-    const bool vec = a.d % 8 == 0 && a.ld_gate % 8 == 0;
-    if (M >= 4 * static_cast<int64_t>(nq_host::sm_count())) E = vec ? 32 : 16;
+    args.err = nq_host::error_word();
+    void* kargs[] = {&args, nullptr, nullptr};
+    const bool row_gate = a.gate && a.ld_gate > 0;
+    const bool shift = a.d % 8 != 0 || a.ld_gate % 8 != 0;
+    if (a.d <= kRingMaxD && M > 2 * static_cast<int64_t>(nq_host::sm_count()) && !(row_gate && a.ld_gate != a.d)) {
+        nq::NormRing ring{};
+        ring.s16[0] = a.y;
+        ring.s16[1] = row_gate ? a.gate : nullptr;
+        ring.sh[0] = a.h;
+        if (plan_ring(ring, a.d, a.h_f32)) {
+            const void* fn = pick(false, shift, a.h_f32, row_gate);
+            if (!fn) return NQ_ERR_LAUNCH;
+            kargs[1] = &ring;
+            kargs[2] = &M;
+            const int64_t blocks = std::min<int64_t>(M, static_cast<int64_t>(ring_blocks_per_sm(a.d)) * nq_host::sm_count());
+            return launched(nq_host::launch_pdl(fn, dim3(static_cast<unsigned>(blocks)), dim3(row_threads(a.d, nq::kRingE)),
+                                                static_cast<size_t>(ring.stages) * ring.stage_bytes, stream, kargs, pdl));
+        }
+    }
     const void* fn = reinterpret_cast<const void*>(nq::block_norm_any_kernel);
     int threads = nq::kNormThreads;
-    if (a.d <= 8192) {
-        fn = vec ? (a.h_f32 ? rows_kernel<true, true>(E) : rows_kernel<true, false>(E))
-                 : (a.h_f32 ? rows_kernel<false, true>(E) : rows_kernel<false, false>(E));
-        threads = row_threads(a.d, E);
+    if (a.d <= 8 * 1024) {
+        fn = shift ? (a.h_f32 ? reinterpret_cast<const void*>(nq::block_norm_rows_kernel<true, true>)
+                              : reinterpret_cast<const void*>(nq::block_norm_rows_kernel<true, false>))
+                   : (a.h_f32 ? reinterpret_cast<const void*>(nq::block_norm_rows_kernel<false, true>)
+                              : reinterpret_cast<const void*>(nq::block_norm_rows_kernel<false, false>));
+        threads = row_threads(a.d, 8);
     }
-    return nq_host::launch_pdl(fn, dim3(static_cast<unsigned>(M)), dim3(threads), 0, stream, kargs, pdl) == cudaSuccess
-               ? NQ_OK
-               : NQ_ERR_LAUNCH;
+    return launched(nq_host::launch_pdl(fn, dim3(static_cast<unsigned>(M)), dim3(threads), 0, stream, kargs, pdl));
 }
 
 size_t nq_block_norm_grad_ws(int64_t d, int64_t M) {
@@ -649,57 +995,24 @@ nq_status nq_launch_block_norm_grad(const nq::NormBwdArgs& a, float* g_w_pre, fl
     sum.d = a.d;
     sum.blocks = blocks;
     const bool row_gate = a.gate && a.ld_gate > 0;
-    bool launched = false;
-    if (a.d <= 512 * nq::kGradE && !(row_gate && a.ld_gate != a.d)) {
-        // rows in shared memory; a row that does not start on 16 bytes brings up to 15 more before and after
-        nq::NormBwdSmem sm{};
-        auto region = [&](bool there, size_t elem) {
-            return there ? static_cast<uint32_t>((a.d * elem + 30 + 127) / 128 * 128) : 0u;
-        };
-        const size_t he = a.h_f32 ? 4 : 2;
-        sm.off_gx = region(a.y != nullptr, 2);
-        sm.off_h = sm.off_gx + region(a.gx != nullptr, 2);
-        sm.off_gh = sm.off_h + region(true, he);
-        sm.off_gate = sm.off_gh + region(a.gh_out != nullptr, he);
-        sm.stage_bytes = sm.off_gate + region(row_gate, 2);
-        const int threads = row_threads(a.d, nq::kGradE);
-        const size_t share = kNormSmemMax / std::max(1, std::min(16, 512 / threads)) - 2048;
-        sm.stages = static_cast<int>(std::max<size_t>(2, std::min<size_t>(4, share / sm.stage_bytes)));
-        if (static_cast<size_t>(sm.stages) * sm.stage_bytes <= kNormSmemMax) {
-            const bool vec = a.d % 8 == 0;
-            const void* fns[4] = {reinterpret_cast<const void*>(nq::block_norm_grad_rows_kernel<false, false>),
-                                  reinterpret_cast<const void*>(nq::block_norm_grad_rows_kernel<false, true>),
-                                  reinterpret_cast<const void*>(nq::block_norm_grad_rows_kernel<true, false>),
-                                  reinterpret_cast<const void*>(nq::block_norm_grad_rows_kernel<true, true>)};
-            static std::atomic<bool> attr_done[64];  // per device; setting an attribute twice is harmless
-            int dev = 0;
-            cudaGetDevice(&dev);
-            if (dev < 0 || dev >= 64) return NQ_ERR_DEVICE;
-            if (!attr_done[dev].load(std::memory_order_acquire)) {
-                for (const void* f : fns)
-                    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kNormSmemMax)) != cudaSuccess)
-                        return NQ_ERR_LAUNCH;
-                attr_done[dev].store(true, std::memory_order_release);
-            }
-            void* kargs[] = {&args, &sm};
-            if (nq_host::launch_pdl(fns[(vec ? 2 : 0) + (a.h_f32 ? 1 : 0)], dim3(blocks), dim3(threads),
-                                    static_cast<size_t>(sm.stages) * sm.stage_bytes, stream, kargs, pdl) != cudaSuccess)
-                return NQ_ERR_LAUNCH;
-            launched = true;
-        }
+    nq::NormRing ring{};
+    ring.s16[0] = a.y;
+    ring.s16[1] = a.gx;
+    ring.s16[2] = row_gate ? a.gate : nullptr;
+    ring.sh[0] = a.h_out;
+    ring.sh[1] = a.gh_out;
+    const void* fn = reinterpret_cast<const void*>(nq::block_norm_grad_any_kernel);
+    int threads = nq::kNormThreads;
+    size_t smem = 0;
+    if (a.d <= kRingMaxD && !(row_gate && a.ld_gate != a.d) && plan_ring(ring, a.d, a.h_f32)) {
+        if (!(fn = pick(true, a.d % 8 != 0, a.h_f32, row_gate))) return NQ_ERR_LAUNCH;
+        threads = row_threads(a.d, nq::kRingE);
+        smem = static_cast<size_t>(ring.stages) * ring.stage_bytes;
     }
-    if (!launched) {
-        void* kargs[] = {&args};
-        if (nq_host::launch_pdl(reinterpret_cast<const void*>(nq::block_norm_grad_any_kernel), dim3(blocks),
-                                dim3(nq::kNormThreads), 0, stream, kargs, pdl) != cudaSuccess)
-            return NQ_ERR_LAUNCH;
-    }
-    if (!any) return NQ_OK;
+    void* kargs[] = {&args, &ring};
+    nq_status st = launched(nq_host::launch_pdl(fn, dim3(blocks), dim3(threads), smem, stream, kargs, pdl));
+    if (st != NQ_OK || !any) return st;
     void* sargs[] = {&sum};
-    return nq_host::launch_pdl(reinterpret_cast<const void*>(nq::norm_vector_sums_kernel),
-                               dim3(static_cast<unsigned>((a.d + 31) / 32), 3), dim3(256), 0, stream, sargs,
-                               pdl) == cudaSuccess
-               ? NQ_OK
-               : NQ_ERR_LAUNCH;
+    return launched(nq_host::launch_pdl(reinterpret_cast<const void*>(nq::norm_vector_sums_kernel),
+                                        dim3(static_cast<unsigned>((a.d + 31) / 32), 3), dim3(256), 0, stream, sargs, pdl));
 }

@@ -18,6 +18,7 @@ struct NormFwdArgs {
     int64_t d, ld_gate;
     float alpha, eps, w_offset;
     bool post, h_f32;
+    unsigned int* err;
 };
 
 struct NormBwdArgs {

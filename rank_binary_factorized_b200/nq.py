@@ -33,6 +33,7 @@ STATUS_NAMES = {0: "NQ_OK", 1: "NQ_ERR_NULL", 2: "NQ_ERR_SHAPE", 3: "NQ_ERR_ALIG
                 9: "NQ_ERR_VALUE", 10: "NQ_ERR_INDEX"}
 MATVEC_MAX_M = 8
 
+_BF16 = torch.bfloat16
 _i64 = ctypes.c_int64
 _p = ctypes.c_void_p
 
@@ -522,43 +523,39 @@ def adapter_rows(ids: torch.Tensor, n: int, stream=None) -> AdapterRows:
     _need(ids, "ids", torch.int32)
     if ids.dim() != 1:
         raise ValueError("ids: expected [M], got shape %s" % (tuple(ids.shape),))
-    with _on(ids.device):
-        rows = torch.empty_like(ids)
-        offsets = torch.empty(max(int(n), 1) + 1, dtype=torch.int32, device=ids.device)
-        _check("nq_adapter_rows", _lib.nq_adapter_rows(_ptr(ids), ids.numel(), int(n), _ptr(rows), _ptr(offsets),
-                                                       _stream_ptr(stream)))
+    rows = torch.empty_like(ids)
+    offsets = torch.empty(max(int(n), 1) + 1, dtype=torch.int32, device=ids.device)
+    _call("nq_adapter_rows", _lib.nq_adapter_rows, ids.device, stream, ids.data_ptr(), ids.numel(), int(n),
+          rows.data_ptr(), offsets.data_ptr())
     return AdapterRows(rows, offsets)
 
 
-class _Here:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def _on(device):
-    """The tensors' device made current for a call (nothing to do where it is already)."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _call(name: str, fn, device, stream, *args) -> None:
+    """Calls the library with the tensors' device current, on `stream` or that device's current one."""
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+    if status != NQ_OK:
+        raise NQError(name, status)
 
 
-def _bf16_rows(t, name: str, M: int, cols: int, device) -> int:
-    """The address of a contiguous [M][cols] bf16 tensor on `device`; _need reports what it is not."""
-    if (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.device == device and
-            t.shape == (M, cols) and t.is_contiguous()):
-        return t.data_ptr()
-    _need(t, name, torch.bfloat16, shape=(M, cols), device=device)
+def _rows_ptr(t, name: str, dtype, M: int, cols: int, device) -> int:
+    """The address of a contiguous [M][cols] tensor on `device`; _need says what is wrong with another."""
+    try:
+        if t.dtype is dtype and t.device == device and t.shape == (M, cols) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape=(M, cols), device=device)
     return t.data_ptr()
 
 
-def _check_groups(ad: Adapters, groups: AdapterRows, M: int) -> None:
-    if groups.M != M or groups.n != ad.n or groups.rows.device != ad.device:
-        raise ValueError("groups: for %d rows and %d adapters on %s, the call has %d, %d and %s" %
-                         (groups.M, groups.n, groups.rows.device, M, ad.n, ad.device))
+def _check_groups(ad: Adapters, groups: AdapterRows) -> None:
+    if groups.n != ad.n or groups.rows.device != ad.device:
+        raise ValueError("groups: for %d adapters on %s, the call has %d on %s" %
+                         (groups.n, groups.rows.device, ad.n, ad.device))
 
 
 def adapter_forward(ad: Adapters, groups: AdapterRows, x: torch.Tensor, y: torch.Tensor, out=None, t=None,
@@ -567,17 +564,15 @@ def adapter_forward(ad: Adapters, groups: AdapterRows, x: torch.Tensor, y: torch
     x [M][d_in], y [M][d_out] bf16; out may be y.  t [M][rank] fp32, if given, receives
     scale_a A_a x[m] for adapter_backward."""
     dev, M = ad.device, groups.M
-    px = _bf16_rows(x, "x", M, ad.d_in, dev)
-    py = _bf16_rows(y, "y", M, ad.d_out, dev)
-    _check_groups(ad, groups, M)
-    with _on(dev):
-        if out is None:
-            out = torch.empty_like(y)
-        po = _bf16_rows(out, "out", M, ad.d_out, dev)
-        if t is not None:
-            _need(t, "t", torch.float32, shape=(M, ad.rank), device=dev)
-        _check("nq_adapter_forward", _lib.nq_adapter_forward(ad._ref, groups._rows_ptr, groups._offsets_ptr, px, py,
-                                                             po, _ptr(t), M, _stream_ptr(stream)))
+    _check_groups(ad, groups)
+    px = _rows_ptr(x, "x", _BF16, M, ad.d_in, dev)
+    py = _rows_ptr(y, "y", _BF16, M, ad.d_out, dev)
+    if out is None:
+        out = torch.empty_like(y)
+    po = _rows_ptr(out, "out", _BF16, M, ad.d_out, dev)
+    pt = 0 if t is None else _rows_ptr(t, "t", torch.float32, M, ad.rank, dev)
+    _call("nq_adapter_forward", _lib.nq_adapter_forward, dev, stream, ad._ref, groups._rows_ptr, groups._offsets_ptr, px,
+          py, po, pt, M)
     return out
 
 
@@ -589,36 +584,33 @@ def adapter_backward(ad: Adapters, groups: AdapterRows, x, ybar: torch.Tensor, t
     [n][rank][d_in], gB [n][d_out][rank] bf16, contiguous.  need_x=False leaves xbar out (xbar may
     be None), need_weights=False leaves gA and gB out (x and t may be None): None in their place."""
     dev, M = ad.device, groups.M
-    pyb = _bf16_rows(ybar, "ybar", M, ad.d_out, dev)
-    _check_groups(ad, groups, M)
+    _check_groups(ad, groups)
+    pyb = _rows_ptr(ybar, "ybar", _BF16, M, ad.d_out, dev)
     px = pt = pxb = po = pa = pb = 0
-    with _on(dev):
-        if need_x:
-            pxb = _bf16_rows(xbar, "xbar", M, ad.d_in, dev)
-            if out is None:
-                out = torch.empty_like(xbar)
-            po = _bf16_rows(out, "out", M, ad.d_in, dev)
-        else:
-            out = None
-        if need_weights:
-            px = _bf16_rows(x, "x", M, ad.d_in, dev)
-            _need(t, "t", torch.float32, shape=(M, ad.rank), device=dev)
-            pt = t.data_ptr()
-            if gA is None:
-                gA = torch.empty((ad.n, ad.rank, ad.d_in), dtype=torch.bfloat16, device=dev)
-            if gB is None:
-                gB = torch.empty((ad.n, ad.d_out, ad.rank), dtype=torch.bfloat16, device=dev)
-            _need(gA, "gA", torch.bfloat16, shape=(ad.n, ad.rank, ad.d_in), device=dev)
-            _need(gB, "gB", torch.bfloat16, shape=(ad.n, ad.d_out, ad.rank), device=dev)
-            pa, pb = gA.data_ptr(), gB.data_ptr()
-        else:
-            gA = gB = None
-        if ws is None:
-            ws = ad.workspace(M)
-        _need_ws(ws, dev)
-        _check("nq_adapter_backward", _lib.nq_adapter_backward(ad._ref, groups._rows_ptr, groups._offsets_ptr, px, pyb,
-                                                               pt, pxb, po, pa, pb, M, ws.data_ptr(), ws.numel(),
-                                                               _stream_ptr(stream)))
+    if need_x:
+        pxb = _rows_ptr(xbar, "xbar", _BF16, M, ad.d_in, dev)
+        if out is None:
+            out = torch.empty_like(xbar)
+        po = _rows_ptr(out, "out", _BF16, M, ad.d_in, dev)
+    else:
+        out = None
+    if need_weights:
+        px = _rows_ptr(x, "x", _BF16, M, ad.d_in, dev)
+        pt = _rows_ptr(t, "t", torch.float32, M, ad.rank, dev)
+        if gA is None:
+            gA = torch.empty((ad.n, ad.rank, ad.d_in), dtype=_BF16, device=dev)
+        if gB is None:
+            gB = torch.empty((ad.n, ad.d_out, ad.rank), dtype=_BF16, device=dev)
+        _need(gA, "gA", _BF16, shape=(ad.n, ad.rank, ad.d_in), device=dev)
+        _need(gB, "gB", _BF16, shape=(ad.n, ad.d_out, ad.rank), device=dev)
+        pa, pb = gA.data_ptr(), gB.data_ptr()
+    else:
+        gA = gB = None
+    if ws is None:
+        ws = ad.workspace(M)
+    _need_ws(ws, dev)
+    _call("nq_adapter_backward", _lib.nq_adapter_backward, dev, stream, ad._ref, groups._rows_ptr, groups._offsets_ptr,
+          px, pyb, pt, pxb, po, pa, pb, M, ws.data_ptr(), ws.numel())
     return out, gA, gB
 
 
@@ -652,13 +644,13 @@ class BlockNorm:
         device = torch.device(device if device is not None else self.device if self.device is not None else "cuda")
         if device.index is None:
             device = torch.device(device.type, torch.cuda.current_device())
-        with _on(device):
+        with torch.cuda.device(device):  # the size goes by the device's multiprocessors
             need = self.workspace_bytes(M)
-            if need == 0:
-                raise NQError("nq_block_norm_workspace_bytes", 2)
-            ws = self._ws.get(device)
-            if ws is None or ws.numel() < need:
-                ws = self._ws[device] = torch.empty(need, dtype=torch.uint8, device=device)
+        if need == 0:
+            raise NQError("nq_block_norm_workspace_bytes", 2)
+        ws = self._ws.get(device)
+        if ws is None or ws.numel() < need:
+            ws = self._ws[device] = torch.empty(need, dtype=torch.uint8, device=device)
         return ws
 
     def _struct(self, h):
@@ -669,14 +661,15 @@ class BlockNorm:
 
 
 def _check_h(norm: BlockNorm, h, name: str):
-    """(M, device) of a residual tensor."""
+    """(M, device, the parameters for h's type) of a residual tensor."""
     if not isinstance(h, torch.Tensor):
         raise TypeError("%s: expected a torch.Tensor, got %s" % (name, type(h).__name__))
     if h.dim() != 2 or h.shape[1] != norm.d:
         raise ValueError("%s: expected [M][%d], got shape %s" % (name, norm.d, tuple(h.shape)))
-    norm._struct(h)
-    _need(h, name, h.dtype, device=norm.device)
-    return int(h.shape[0]), h.device
+    params = norm._struct(h)
+    if not h.is_cuda or not h.is_contiguous() or (norm.device is not None and norm.device != h.device):
+        _need(h, name, h.dtype, device=norm.device)
+    return h.shape[0], h.device, params
 
 
 def _check_gate(norm: BlockNorm, gate, M: int, device):
@@ -684,12 +677,12 @@ def _check_gate(norm: BlockNorm, gate, M: int, device):
     if gate is None:
         return 0, 0
     if isinstance(gate, torch.Tensor) and gate.dim() == 2:
-        _need_rows(gate, "gate", torch.bfloat16, M, norm.d, device=device)
+        _need_rows(gate, "gate", _BF16, M, norm.d, device=device)
         if gate.shape[1] != norm.d or gate.stride(0) < norm.d and M > 1:
             raise ValueError("gate: expected [%d] or [%d][%d], got shape %s strides %s" %
                              (norm.d, M, norm.d, tuple(gate.shape), tuple(gate.stride())))
         return gate.data_ptr(), max(int(gate.stride(0)), norm.d)
-    _need(gate, "gate", torch.bfloat16, shape=(norm.d,), device=device)
+    _need(gate, "gate", _BF16, shape=(norm.d,), device=device)
     return gate.data_ptr(), 0
 
 
@@ -697,19 +690,17 @@ def block_norm(norm: BlockNorm, y, h: torch.Tensor, gate=None, h_out=None, x=Non
     """(h_out, x): h_out = alpha h + gate * z with z the (normed) block output y, x the normed h_out
     for the next block.  y [M][d] bf16 or None, h [M][d] bf16 or fp32, gate [d] or [M][d] bf16 or
     None.  h_out may be h, x may be y."""
-    M, dev = _check_h(norm, h, "h")
-    py = 0 if y is None else _bf16_rows(y, "y", M, norm.d, dev)
+    M, dev, params = _check_h(norm, h, "h")
+    d = norm.d
+    py = 0 if y is None else _rows_ptr(y, "y", _BF16, M, d, dev)
     pg, ldg = _check_gate(norm, gate, M, dev)
-    with _on(dev):
-        if h_out is None:
-            h_out = torch.empty_like(h)
-        elif h_out is not h:
-            _need(h_out, "h_out", h.dtype, shape=(M, norm.d), device=dev)
-        if x is None:
-            x = torch.empty((M, norm.d), dtype=torch.bfloat16, device=dev)
-        px = _bf16_rows(x, "x", M, norm.d, dev)
-        _check("nq_block_norm_forward", _lib.nq_block_norm_forward(norm._struct(h), py, h.data_ptr(), pg, ldg,
-                                                                   h_out.data_ptr(), px, M, _stream_ptr(stream)))
+    if h_out is None:
+        h_out = torch.empty_like(h)
+    ph = _rows_ptr(h_out, "h_out", h.dtype, M, d, dev)
+    if x is None:
+        x = torch.empty((M, d), dtype=_BF16, device=dev)
+    px = _rows_ptr(x, "x", _BF16, M, d, dev)
+    _call("nq_block_norm_forward", _lib.nq_block_norm_forward, dev, stream, params, py, h.data_ptr(), pg, ldg, ph, px, M)
     return h_out, x
 
 
@@ -721,49 +712,42 @@ def block_norm_backward(norm: BlockNorm, y, h_out: torch.Tensor, gx, gh_out, gat
     w_pre; need_weights=False leaves g_w_pre, g_w_post and a shared gate's g_gate out.  g_w_pre,
     g_w_post and the g_gate of one shared gate are fp32 [d], the g_gate of a gate per row bf16
     [M][d].  gh may be gh_out, gy may be gx."""
-    M, dev = _check_h(norm, h_out, "h_out")
+    M, dev, params = _check_h(norm, h_out, "h_out")
     d = norm.d
-    py = 0 if y is None else _bf16_rows(y, "y", M, d, dev)
-    pgx = 0 if gx is None else _bf16_rows(gx, "gx", M, d, dev)
+    py = 0 if y is None else _rows_ptr(y, "y", _BF16, M, d, dev)
+    pgx = 0 if gx is None else _rows_ptr(gx, "gx", _BF16, M, d, dev)
     pg, ldg = _check_gate(norm, gate, M, dev)
-    if gh_out is not None:
-        _need(gh_out, "gh_out", h_out.dtype, shape=(M, d), device=dev)
+    pgo = 0 if gh_out is None else _rows_ptr(gh_out, "gh_out", h_out.dtype, M, d, dev)
 
     def vector(v, name, wanted):
         if not wanted:
-            return None
+            return None, 0
         if v is None:
-            return torch.empty(d, dtype=torch.float32, device=dev)
+            v = torch.empty(d, dtype=torch.float32, device=dev)
         _need(v, name, torch.float32, shape=(d,), device=dev)
-        return v
+        return v, v.data_ptr()
 
-    with _on(dev):
-        if gh is None:
-            gh = torch.empty_like(h_out)
-        _need(gh, "gh", h_out.dtype, shape=(M, d), device=dev)
-        if y is None:
-            gy = None
-        else:
-            if gy is None:
-                gy = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
-            _bf16_rows(gy, "gy", M, d, dev)
-        g_w_pre = vector(g_w_pre, "g_w_pre", need_weights and norm.w_pre is not None)
-        g_w_post = vector(g_w_post, "g_w_post", need_weights and norm.post_norm and norm.w_post is not None and
-                          y is not None)
-        if gate is None or y is None:
-            g_gate = None
-        elif ldg == 0:
-            g_gate = vector(g_gate, "g_gate", need_weights)
-        else:
-            if g_gate is None:
-                g_gate = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
-            _bf16_rows(g_gate, "g_gate", M, d, dev)
-        if ws is None:
-            ws = norm.workspace(M, dev)
-        _need_ws(ws, dev)
-        _check("nq_block_norm_backward", _lib.nq_block_norm_backward(
-            norm._struct(h_out), py, h_out.data_ptr(), pg, ldg, pgx, _ptr(gh_out), gh.data_ptr(), _ptr(gy),
-            _ptr(g_w_pre), _ptr(g_w_post), _ptr(g_gate), M, ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+    def rows(v, name, dtype):
+        if v is None:
+            v = torch.empty((M, d), dtype=dtype, device=dev)
+        return v, _rows_ptr(v, name, dtype, M, d, dev)
+
+    gh, pgh = rows(gh, "gh", h_out.dtype)
+    gy, pgy = (None, 0) if y is None else rows(gy, "gy", _BF16)
+    g_w_pre, pwp = vector(g_w_pre, "g_w_pre", need_weights and norm.w_pre is not None)
+    g_w_post, pwo = vector(g_w_post, "g_w_post",
+                           need_weights and norm.post_norm and norm.w_post is not None and y is not None)
+    if gate is None or y is None:
+        g_gate, pgg = None, 0
+    elif ldg == 0:
+        g_gate, pgg = vector(g_gate, "g_gate", need_weights)
+    else:
+        g_gate, pgg = rows(g_gate, "g_gate", _BF16)
+    if ws is None:
+        ws = norm.workspace(M, dev)
+    _need_ws(ws, dev)
+    _call("nq_block_norm_backward", _lib.nq_block_norm_backward, dev, stream, params, py, h_out.data_ptr(), pg, ldg, pgx,
+          pgo, pgh, pgy, pwp, pwo, pgg, M, ws.data_ptr(), ws.numel())
     return gh, gy, g_w_pre, g_w_post, g_gate
 
 
