@@ -39,12 +39,75 @@ __device__ __forceinline__ void ld_bf16(const uint16_t* p, float (&v)[V]) {
 
 struct RowsShared {
     alignas(16) uint16_t z[kRowsTile][kRowsChunk];
-    float part[kRowsTile][kMaxRank];  // this block's share of t
-    float t[kRowsTile][kMaxRank];     // t, scaled
-    float red[kRowsThreads * kRowsTile];
+    alignas(16) float part[kRowsTile][kMaxRank];  // this block's share of t
+    alignas(16) float t[kRowsTile][kMaxRank];     // t, scaled
+    float warp_part[kRowsThreads / 32][kRowsTile][kMaxRank];  // BWD: by warp
     int row[kRowsTile];
     AdapterTile tile;
 };
+
+// out_i = base_i + sum_r B[i][r] t_r for rows of B of over 32 bytes: G lanes share a row (16 bytes of it
+// each at a time), so that a warp reads whole lines, and a lane has G rows' loads in flight.  The
+// lanes' sums are exchanged by halves: lane g of the G ends with the sum of its g-th row.
+template <int G, int NT>
+__device__ __forceinline__ void rows_expand(const AdapterArgs& a, RowsShared& s, const uint16_t* B, int64_t n_begin,
+                                            int64_t n_end) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G, sub = lane / G, R = a.rank;
+    const int count = s.tile.count;
+    for (int64_t i0 = n_begin + warp * 32; i0 < n_end; i0 += kRowsThreads) {
+        const int64_t mine = i0 + g * (32 / G) + sub, at = min(mine, n_end - 1);
+        uint16_t old[NT];
+        float acc[NT][G];
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+            old[m] = a.base[max(m < count ? s.row[m] : 0, 0) * a.N + at];
+#pragma unroll
+            for (int j = 0; j < G; ++j) acc[m][j] = 0.f;
+        }
+        for (int r0 = 0; r0 < R; r0 += 8 * G) {
+            const int r = r0 + g * 8;
+            uint4 w[G];
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                w[j] = *reinterpret_cast<const uint4*>(B + min(i0 + j * (32 / G) + sub, n_end - 1) * a.ldb + min(r, R - 8));
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                float t[8];
+                *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(&s.t[m][min(r, R - 8)]);
+                *reinterpret_cast<float4*>(t + 4) = *reinterpret_cast<const float4*>(&s.t[m][min(r, R - 8) + 4]);
+                if (r >= R) {  // past the rank: counts nothing
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const uint32_t ww[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                    float sum = acc[m][j];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum = fmaf(__uint_as_float(ww[e] << 16), t[2 * e], sum);
+                        sum = fmaf(__uint_as_float(ww[e] & 0xFFFF0000u), t[2 * e + 1], sum);
+                    }
+                    acc[m][j] = r < R ? sum : acc[m][j];
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+#pragma unroll
+            for (int o = G / 2; o >= 1; o /= 2) {
+                const bool upper = g & o;
+#pragma unroll
+                for (int j = 0; j < o; ++j) {
+                    const float keep = upper ? acc[m][j + o] : acc[m][j], give = upper ? acc[m][j] : acc[m][j + o];
+                    acc[m][j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                }
+            }
+            if (mine < n_end && m < count && s.row[m] >= 0)
+                a.out[s.row[m] * a.N + mine] = float_to_bf16_bits(bf16_bits_to_float(old[m]) + acc[m][0]);
+        }
+    }
+}
 
 // NT rows at most (1, 2, 4 or 8: the loops over rows are unrolled).  V = 8: every row of A, B, z
 // and base starts on 16 bytes and every width is a multiple of 8; V = 1: any.
@@ -63,61 +126,75 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
         const int64_t k_begin = min(a.K, per * q), k_end = min(a.K, k_begin + per);
         for (int64_t k0 = k_begin; k0 < k_end; k0 += kRowsChunk) {
             const int len = static_cast<int>(min(static_cast<int64_t>(kRowsChunk), k_end - k0));
-#pragma unroll
-            for (int m = 0; m < NT; ++m) {
-                const int row = m < count ? s.row[m] : -1;
-                for (int k = threadIdx.x * V; k < len; k += kRowsThreads * V) {
-                    if constexpr (V == 8) {
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (row >= 0) w = *reinterpret_cast<const uint4*>(a.z + row * a.K + k0 + k);
-                        *reinterpret_cast<uint4*>(&s.z[m][k]) = w;
-                    } else {
-                        s.z[m][k] = row >= 0 ? a.z[row * a.K + k0 + k] : static_cast<uint16_t>(0);
-                    }
+            // rows that are not there read row 0 and count as zeros
+            const int vecs = len / V;
+#pragma unroll 4
+            for (int e = threadIdx.x; e < NT * vecs; e += kRowsThreads) {
+                const int m = e / vecs, k = (e - m * vecs) * V, row = m < count ? s.row[m] : -1;
+                const uint16_t* from = a.z + max(row, 0) * a.K + k0 + k;
+                if constexpr (V == 8) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(from);
+                    *reinterpret_cast<uint4*>(&s.z[m][k]) = row >= 0 ? w : make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    const uint16_t w = *from;
+                    s.z[m][k] = row >= 0 ? w : static_cast<uint16_t>(0);
                 }
             }
             __syncthreads();
             if constexpr (!BWD) {
-                // warp w: t_r for r = w, w + 8, ...; lanes along K
-                for (int r = warp; r < R; r += kRowsThreads / 32) {
-                    const uint16_t* w = A + r * a.lda + k0;
-                    float acc[NT];
+                // warp w: t_r for r = w, w + 8, ..., kSide of them at once; lanes along K
+                constexpr int kSide = NT <= 2 ? 4 : 2, kWarps = kRowsThreads / 32;
+                for (int rb = warp; rb < R; rb += kSide * kWarps) {
+                    float acc[kSide][NT];
 #pragma unroll
-                    for (int m = 0; m < NT; ++m) acc[m] = 0.f;
-#pragma unroll 4
+                    for (int j = 0; j < kSide; ++j)
+#pragma unroll
+                        for (int m = 0; m < NT; ++m) acc[j][m] = 0.f;
+#pragma unroll 2
                     for (int k = lane * V; k < len; k += 32 * V) {
-                        float wv[V];
-                        ld_bf16<V>(w + k, wv);
+                        float wv[kSide][V];
+#pragma unroll
+                        for (int j = 0; j < kSide; ++j) {
+                            const int r = min(rb + j * kWarps, R - 1);  // past the last: read again, not stored
+                            ld_bf16<V>(A + r * a.lda + k0 + k, wv[j]);
+                        }
 #pragma unroll
                         for (int m = 0; m < NT; ++m) {
                             float zv[V];
                             ld_bf16<V>(&s.z[m][k], zv);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) acc[m] = fmaf(wv[i], zv[i], acc[m]);
+                            for (int j = 0; j < kSide; ++j)
+#pragma unroll
+                                for (int i = 0; i < V; ++i) acc[j][m] = fmaf(wv[j][i], zv[i], acc[j][m]);
                         }
                     }
 #pragma unroll
-                    for (int m = 0; m < NT; ++m) {
+                    for (int j = 0; j < kSide; ++j)
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
-                        if (lane == 0) s.part[m][r] += acc[m];  // (m, r) belongs to this warp
-                    }
+                        for (int m = 0; m < NT; ++m) {
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) acc[j][m] += __shfl_xor_sync(0xFFFFFFFFu, acc[j][m], o);
+                            const int r = rb + j * kWarps;
+                            if (lane == 0 && r < R) s.part[m][r] += acc[j][m];  // (m, r) belongs to this warp
+                        }
                 }
             } else {
-                // u_r = sum_k z_k B[k][r]: threads side by side along r, groups of them along K
-                const int rv = (R + V - 1) / V;          // vectors of r in a row of B
-                const int side = min(rv, kRowsThreads);  // threads along r
-                const int groups = kRowsThreads / side;
-                const int g = threadIdx.x / side, v0 = threadIdx.x % side;
+                // u_r = sum_k z_k B[k][r]: `side` lanes (a power of two) side by side along r, the warp's
+                // other lanes and the warps along K
+                const int rv = (R + V - 1) / V;  // vectors of r in a row of B
+                int side = 1;
+                while (side < rv && side < 32) side *= 2;
+                const int along = 32 / side, g = warp * along + lane / side, groups = kRowsThreads / 32 * along;
                 for (int vb = 0; vb < rv; vb += side) {
-                    const int r0 = (vb + v0) * V;
+                    const int r0 = (vb + lane % side) * V;
                     float acc[NT][V];
 #pragma unroll
                     for (int m = 0; m < NT; ++m)
 #pragma unroll
                         for (int i = 0; i < V; ++i) acc[m][i] = 0.f;
-                    if (g < groups && r0 < R) {
-#pragma unroll 4
+                    if (r0 < R) {
+                        constexpr int kUnroll = NT <= 2 ? 8 : 4;
+#pragma unroll kUnroll
                         for (int k = g; k < len; k += groups) {
                             float wv[V];
                             ld_bf16<V>(B + (k0 + k) * a.ldb + r0, wv);
@@ -129,22 +206,20 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
                             }
                         }
                     }
-                    // the groups' sums meet in shared memory, one row and one element of V at a time
 #pragma unroll
-                    for (int m = 0; m < NT; ++m) {
+                    for (int m = 0; m < NT; ++m)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) s.red[threadIdx.x * V + i] = acc[m][i];
-                        __syncthreads();
-                        for (int e = threadIdx.x; e < side * V; e += kRowsThreads) {
-                            const int r = vb * V + e;
-                            if (r < R) {
-                                float sum = 0.f;
-                                for (int gg = 0; gg < groups; ++gg) sum += s.red[gg * side * V + e];
-                                s.part[m][r] += sum;
-                            }
+                        for (int i = 0; i < V; ++i) {
+                            for (int o = 16; o >= side; o /= 2) acc[m][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[m][i], o);
+                            if (lane < side && r0 + i < R) s.warp_part[warp][m][r0 + i] = acc[m][i];
                         }
-                        __syncthreads();
-                    }
+                }
+                __syncthreads();
+                for (int e = threadIdx.x; e < NT * R; e += kRowsThreads) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kRowsThreads / 32; ++w) sum += s.warp_part[w][e / R][e % R];
+                    s.part[e / R][e % R] += sum;
                 }
             }
             __syncthreads();  // z is rewritten by the next chunk
@@ -172,6 +247,30 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
             if (row >= 0) a.t[static_cast<int64_t>(row) * R + e % R] = none ? 0.f : s.t[e / R][e % R];
         }
     }
+    if constexpr (BWD) {
+        if ((a.u_parts || a.t_parts) && !none && q == 0) {
+            // this tile's padded rows; the group's last tile also zeroes those up to a multiple of 16
+            const bool last = s.tile.first + count == a.offsets[adapter + 1];
+            const int rows = last ? ((s.tile.padded + count + 15) & ~15) - s.tile.padded : kRowsTile;
+            const int64_t part = a.part_rows * a.part_ld;
+            for (int e = threadIdx.x; e < rows * a.part_ld; e += kRowsThreads) {
+                const int m = e / a.part_ld, r = e % a.part_ld;
+                const bool there = m < count && r < R;
+                const int64_t at = (static_cast<int64_t>(s.tile.padded) + m) * a.part_ld + r;
+                auto put = [&](uint16_t* to, float v) {
+                    const uint16_t hi = float_to_bf16_bits(v);
+                    const float h = bf16_bits_to_float(hi);
+                    to[at] = hi;
+                    to[at + part] = float_to_bf16_bits(isinf(h) ? 0.f : v - h);
+                };
+                if (a.u_parts) put(a.u_parts, there ? s.t[m][r] : 0.f);
+                if (a.t_parts) {
+                    const int row = there ? s.row[m] : -1;
+                    put(a.t_parts, row >= 0 ? a.t_in[static_cast<int64_t>(row) * R + r] : 0.f);
+                }
+            }
+        }
+    }
     if (a.out && !(none && a.out == a.base)) {
         const int64_t per = ((a.N + nq - 1) / nq + 7) / 8 * 8;
         const int64_t n_begin = min(a.N, per * q), n_end = min(a.N, n_begin + per);
@@ -188,66 +287,131 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
                 }
             }
         } else if constexpr (!BWD) {
-            // out_i = base_i + sum_r B[i][r] t_r: G lanes share a row of B, each with every G-th vector
-            const int rv = (R + V - 1) / V;
-            int G = 1;
-            while (G < rv && G < 32) G *= 2;
-            const int gl = lane % G, rows_per_pass = kRowsThreads / G;
-            for (int64_t i0 = n_begin; i0 < n_end; i0 += rows_per_pass) {
-                const int64_t i = i0 + threadIdx.x / G;
-                float acc[NT];
-#pragma unroll
-                for (int m = 0; m < NT; ++m) acc[m] = 0.f;
-                if (i < n_end) {
-                    for (int v = gl; v < rv; v += G) {
-                        float wv[V];
-                        ld_bf16<V>(B + i * a.ldb + v * V, wv);
-#pragma unroll
-                        for (int m = 0; m < NT; ++m)
-#pragma unroll
-                            for (int e = 0; e < V; ++e) acc[m] = fmaf(wv[e], s.t[m][v * V + e], acc[m]);
-                    }
+            if constexpr (V == 8) {
+                if (R > 32) {
+                    rows_expand<(NT <= 4 ? 8 : 4), NT>(a, s, B, n_begin, n_end);  // registers: G NT sums
+                } else if (R > 16) {
+                    rows_expand<4, NT>(a, s, B, n_begin, n_end);
                 }
+            }
+            // out_i = base_i + sum_r B[i][r] t_r: a thread has a row of B at a time, kAhead rows' loads in
+            // flight; neighbouring threads neighbouring i
+            constexpr int kAhead = NT <= 2 ? 4 : 2, kPiece = V == 8 ? 2 : 8;  // vectors of a row loaded at once
+            for (int64_t i0 = n_begin + threadIdx.x; (V != 8 || R <= 16) && i0 < n_end; i0 += kAhead * kRowsThreads) {
+                float acc[kAhead][NT];
+                uint16_t old[kAhead][NT];
 #pragma unroll
-                for (int m = 0; m < NT; ++m)
-                    for (int o = G / 2; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
-                if (i < n_end) {
+                for (int h = 0; h < kAhead; ++h)
 #pragma unroll
                     for (int m = 0; m < NT; ++m) {
-                        if (m % G == gl && m < count && s.row[m] >= 0) {
-                            const int64_t at = s.row[m] * a.N + i;
-                            a.out[at] = float_to_bf16_bits(bf16_bits_to_float(a.base[at]) + acc[m]);
+                        const int64_t i = min(i0 + h * kRowsThreads, n_end - 1);
+                        acc[h][m] = 0.f;
+                        old[h][m] = a.base[max(m < count ? s.row[m] : 0, 0) * a.N + i];
+                    }
+                for (int r0 = 0; r0 < R; r0 += kPiece * V) {
+                    float w[kAhead][kPiece][V];
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+                        for (int v = 0; v < kPiece; ++v) {
+                            const int64_t i = min(i0 + h * kRowsThreads, n_end - 1);
+                            ld_bf16<V>(B + i * a.ldb + min(r0 + v * V, R - V), w[h][v]);
+                        }
+#pragma unroll
+                    for (int v = 0; v < kPiece; ++v) {
+                        if (r0 + v * V >= R) break;  // the same for every thread
+#pragma unroll
+                        for (int m = 0; m < NT; ++m) {
+                            float t[V];
+                            if constexpr (V == 8) {
+                                *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(&s.t[m][r0 + v * V]);
+                                *reinterpret_cast<float4*>(t + 4) = *reinterpret_cast<const float4*>(&s.t[m][r0 + v * V + 4]);
+                            } else {
+                                t[0] = s.t[m][r0 + v];
+                            }
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+#pragma unroll
+                                for (int h = 0; h < kAhead; ++h) acc[h][m] = fmaf(w[h][v][e], t[e], acc[h][m]);
                         }
                     }
                 }
+#pragma unroll
+                for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+                    for (int m = 0; m < NT; ++m) {
+                        const int64_t i = i0 + h * kRowsThreads;
+                        if (i < n_end && m < count && s.row[m] >= 0)
+                            a.out[s.row[m] * a.N + i] = float_to_bf16_bits(bf16_bits_to_float(old[h][m]) + acc[h][m]);
+                    }
             }
         } else {
-            // out_j = base_j + sum_r u_r A[r][j]: a thread holds V neighbouring j
-            for (int64_t j = n_begin + threadIdx.x * V; j < n_end; j += kRowsThreads * V) {
+            // out_j = base_j + sum_r u_r A[r][j]: a thread holds V neighbouring j; where that leaves threads
+            // over, groups of threads share the ranks and add up in shared memory
+            const int vecs = static_cast<int>((n_end - n_begin + V - 1) / V);
+            int share = 1;
+            while (V == 8 && share < 8 && 2 * share * vecs <= kRowsThreads) share *= 2;
+            const int per = kRowsThreads / share, g = threadIdx.x / per;
+            float* sums = &s.warp_part[0][0][0];  // [share][per][V]
+            for (int v0 = 0; v0 < vecs; v0 += per) {
+                const int64_t j = n_begin + static_cast<int64_t>(v0 + threadIdx.x % per) * V;
+                const bool in = j < n_end;
                 float acc[NT][V];
+                alignas(16) uint16_t old[NT][V];
 #pragma unroll
                 for (int m = 0; m < NT; ++m)
 #pragma unroll
                     for (int i = 0; i < V; ++i) acc[m][i] = 0.f;
-#pragma unroll 4
-                for (int r = 0; r < R; ++r) {
-                    float wv[V];
-                    ld_bf16<V>(A + r * a.lda + j, wv);
+                if (in && g == 0) {
 #pragma unroll
                     for (int m = 0; m < NT; ++m) {
-                        const float u = s.t[m][r];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) acc[m][i] = fmaf(u, wv[i], acc[m][i]);
+                        const uint16_t* from = a.base + max(m < count ? s.row[m] : 0, 0) * a.N + j;
+                        if constexpr (V == 8)
+                            *reinterpret_cast<uint4*>(old[m]) = *reinterpret_cast<const uint4*>(from);
+                        else
+                            old[m][0] = *from;
                     }
                 }
+                if (in) {
+                    constexpr int kUnroll = NT <= 2 ? 8 : 4;
+#pragma unroll kUnroll
+                    for (int r = g; r < R; r += share) {
+                        float wv[V];
+                        ld_bf16<V>(A + r * a.lda + j, wv);
 #pragma unroll
-                for (int m = 0; m < NT; ++m) {
-                    if (m < count && s.row[m] >= 0) {
-                        const int64_t at = s.row[m] * a.N + j;
-                        float bv[V];
-                        ld_bf16<V>(a.base + at, bv);
+                        for (int m = 0; m < NT; ++m) {
+                            const float u = s.t[m][r];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) a.out[at + i] = float_to_bf16_bits(bv[i] + acc[m][i]);
+                            for (int i = 0; i < V; ++i) acc[m][i] = fmaf(u, wv[i], acc[m][i]);
+                        }
+                    }
+                }
+                if (share > 1) {
+#pragma unroll
+                    for (int m = 0; m < NT; ++m) {
+                        __syncthreads();
+#pragma unroll
+                        for (int i = 0; i < V; ++i) sums[threadIdx.x * V + i] = acc[m][i];
+                        __syncthreads();
+                        if (g == 0)
+                            for (int h = 1; h < share; ++h)
+#pragma unroll
+                                for (int i = 0; i < V; ++i) acc[m][i] += sums[(h * per + threadIdx.x) * V + i];
+                    }
+                }
+                if (in && g == 0) {
+#pragma unroll
+                    for (int m = 0; m < NT; ++m) {
+                        if (m < count && s.row[m] >= 0) {
+                            alignas(16) uint16_t now[V];
+#pragma unroll
+                            for (int i = 0; i < V; ++i) now[i] = float_to_bf16_bits(bf16_bits_to_float(old[m][i]) + acc[m][i]);
+                            uint16_t* to = a.out + s.row[m] * a.N + j;
+                            if constexpr (V == 8)
+                                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(now);
+                            else
+                                *to = now[0];
+                        }
                     }
                 }
             }
@@ -257,7 +421,7 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
 }
 
 template <bool BWD, int V>
-__global__ void __launch_bounds__(kRowsThreads) adapter_rows_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, 2) adapter_rows_kernel(const AdapterArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     RowsShared& s = *reinterpret_cast<RowsShared*>(smem_raw);
     pdl_wait();
@@ -400,14 +564,18 @@ nq_status nq_launch_adapter_rows(const nq::AdapterArgs& a, bool backward, cudaSt
     if (dev < 0 || dev >= 64) return NQ_ERR_DEVICE;
     if (!attr_done[dev].load(std::memory_order_acquire)) {
         for (const void* f : fns)
-            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(nq::RowsShared)) != cudaSuccess)
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(nq::RowsShared)) != cudaSuccess ||
+                cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
                 return NQ_ERR_LAUNCH;
         attr_done[dev].store(true, std::memory_order_release);
     }
     const int64_t tiles = nq::max_adapter_tiles(a.M, a.n, nq::kRowsTile, nq::kRowsTile);
-    // blocks per tile: enough to give every multiprocessor one, at most a portable cluster
-    int cs = 8;
-    while (cs > 1 && tiles * cs > 2 * static_cast<int64_t>(nq_host::sm_count())) cs /= 2;
+    // blocks per tile: what two blocks a multiprocessor have room for, 16 at most (a cluster of 16 needs
+    // the multiprocessors of one GPC: only where the tiles are few)
+    const int64_t sms = nq_host::sm_count();
+    int cs = 16;
+    if (tiles * cs > sms / 2) cs = 8;
+    while (cs > 1 && tiles * cs > 2 * sms) cs /= 2;
     void* kargs[] = {&args};
     return nq_host::launch_ex(fns[(backward ? 2 : 0) + (vec ? 1 : 0)],
                               dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(cs)), dim3(nq::kRowsThreads),

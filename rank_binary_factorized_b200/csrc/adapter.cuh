@@ -73,19 +73,28 @@ __device__ __forceinline__ void adapter_bounds(const int32_t* offsets, int n, in
 }
 
 // Tile number `tile` when every adapter's rows are cut into tiles of rows_per_tile and those
-// without one into tiles of none_per_tile, groups in order.  A whole warp calls it; 32 groups are
-// scanned at a time.
+// without one into tiles of none_per_tile, groups in order.  A whole warp calls it; 128 groups are
+// scanned at a time, four neighbours a lane.
 __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, int64_t M, int rows_per_tile,
                                                  int none_per_tile, int tile, unsigned int* err) {
     const int lane = threadIdx.x & 31;
-    int before = 0;  // tiles of the groups before this batch of 32
+    int before = 0;  // tiles of the groups before this batch
     int padded = 0;  // and their rows in multiples of 16
-    for (int a0 = 0; a0 <= n; a0 += 32) {
-        const int a = a0 + lane;
-        int first = 0, last = 0;
-        if (a <= n) adapter_bounds(offsets, n, M, a, first, last, err);
-        const int per = a < n ? rows_per_tile : none_per_tile;
-        const int mine = (last - first + per - 1) / per;
+    for (int a0 = 0; a0 <= n; a0 += 128) {
+        int first[4], last[4], tiles[4], mine = 0, rows16 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int a = a0 + 4 * lane + i;
+            first[i] = last[i] = 0;
+            if (a <= n) adapter_bounds(offsets, n, M, a, first[i], last[i], err);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int per = a0 + 4 * lane + i < n ? rows_per_tile : none_per_tile;
+            tiles[i] = (last[i] - first[i] + per - 1) / per;
+            mine += tiles[i];
+            rows16 += (last[i] - first[i] + 15) & ~15;
+        }
         int upto = mine;  // inclusive sum over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -97,17 +106,33 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
         if (hit) {
             const int src = __ffs(hit) - 1;
             AdapterTile t;
-            t.adapter = a0 + src;
-            const int off = (local - (__shfl_sync(0xFFFFFFFFu, upto, src) - __shfl_sync(0xFFFFFFFFu, mine, src))) *
-                            (t.adapter < n ? rows_per_tile : none_per_tile);
-            t.first = __shfl_sync(0xFFFFFFFFu, first, src) + off;
-            t.padded = padded + static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < src ? (last - first + 15) & ~15 : 0)) +
-                       off;
-            t.count = min(t.adapter < n ? rows_per_tile : none_per_tile, __shfl_sync(0xFFFFFFFFu, last, src) - t.first);
+            t.padded = padded + static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < src ? rows16 : 0));
+            // the lane that has it looks through its four groups
+            int rest = local - (upto - mine);
+            t.adapter = -1;
+            t.first = t.count = 0;
+            int in_lane = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (t.adapter < 0 && rest < tiles[i]) {
+                    const int per = a0 + 4 * lane + i < n ? rows_per_tile : none_per_tile;
+                    t.adapter = a0 + 4 * lane + i;
+                    t.first = first[i] + rest * per;
+                    t.count = min(per, last[i] - t.first);
+                    in_lane += rest * per;
+                } else if (t.adapter < 0) {
+                    rest -= tiles[i];
+                    in_lane += (last[i] - first[i] + 15) & ~15;
+                }
+            }
+            t.adapter = __shfl_sync(0xFFFFFFFFu, t.adapter, src);
+            t.first = __shfl_sync(0xFFFFFFFFu, t.first, src);
+            t.count = __shfl_sync(0xFFFFFFFFu, t.count, src);
+            t.padded += __shfl_sync(0xFFFFFFFFu, in_lane, src);
             return t;
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
-        padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, (last - first + 15) & ~15));
+        padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rows16));
     }
     return {-1, 0, 0, 0};
 }

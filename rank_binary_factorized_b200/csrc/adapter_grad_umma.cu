@@ -23,6 +23,7 @@ constexpr int kWgTok = 64;                  // tokens of a slot
 constexpr uint32_t kWgPanel = kWgTok * 128; // 64 tokens x 64 bf16
 constexpr int kWgThreads = 192;
 constexpr int kWgMaxSlots = 4;
+constexpr int kWgGroups = 1024;             // groups whose bounds are kept in shared memory
 
 struct AdapterWgradArgs {
     AdapterGradArgs g;
@@ -32,6 +33,9 @@ struct AdapterWgradArgs {
     uint32_t slot_bytes;
     int panels, r16;
     uint32_t acc_cols;        // TMEM columns of one accumulator pair
+    int splits;               // blocks that share the tokens of a unit
+    float* partial;           // splits > 1: [splits] sums of gA [n][rank][d_in], then of gB [n][d_out][rank]
+    int64_t split_stride, gb_at;
 };
 
 __global__ void __launch_bounds__(kWgThreads, 1)
@@ -50,6 +54,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto acc_full = [&](int i) { return bars + 8u * (2 * kWgMaxSlots + i); };
     auto acc_empty = [&](int i) { return bars + 8u * (2 * kWgMaxSlots + 2 + i); };
     const uint32_t drain = bars + 8u * (2 * kWgMaxSlots + 4), tmem_slot = drain + 8u;
+    // bounds of every adapter's rows (where there are not too many): first, last, first padded row
+    int(*const bounds)[3] = reinterpret_cast<int(*)[3]>(smem_raw + (bars + 128u - tc::smem_u32(smem_raw)));
+    const bool kept = g.n <= kWgGroups;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* err = g.err;
 
@@ -75,9 +82,44 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
     const int per_adapter = wa.in_tiles + wa.out_tiles;
-    const int64_t units = static_cast<int64_t>(per_adapter) * g.n;
+    const int64_t units = static_cast<int64_t>(per_adapter) * g.n * wa.splits;
+    // tokens of split sp of a group, in slots
+    auto share = [&](int rows, int sp, int& b0, int& b1) {
+        const int64_t all = (rows + kWgTok - 1) / kWgTok;
+        b0 = static_cast<int>(all * sp / wa.splits);
+        b1 = static_cast<int>(all * (sp + 1) / wa.splits);
+    };
     pdl_wait();
     pdl_launch_dependents();
+    if (kept) {
+        if (warp == 0) {
+            int padded = 0;
+            for (int a0 = 0; a0 < g.n; a0 += 32) {
+                int first = 0, last = 0;
+                if (a0 + lane < g.n) adapter_bounds(g.offsets, g.n, g.M, a0 + lane, first, last, err);
+                const int rows16 = (last - first + 15) & ~15;
+                int upto = rows16;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                if (a0 + lane < g.n) {
+                    bounds[a0 + lane][0] = first;
+                    bounds[a0 + lane][1] = last;
+                    bounds[a0 + lane][2] = padded + upto - rows16;
+                }
+                padded += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            }
+        }
+        __syncthreads();
+    }
+    auto group = [&](int adapter, int& first, int& last) {  // returns the first padded row (warp-wide)
+        if (!kept) return find_group(g.offsets, g.n, g.M, adapter, first, last, err);
+        first = bounds[adapter][0];
+        last = bounds[adapter][1];
+        return bounds[adapter][2];
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
@@ -85,26 +127,37 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         int s = 0;
         bool ok = true;
         for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
-            const int adapter = static_cast<int>(unit / per_adapter), tile = static_cast<int>(unit % per_adapter);
+            const int sp = static_cast<int>(unit % wa.splits);
+            const int adapter = static_cast<int>(unit / wa.splits / per_adapter);
+            const int tile = static_cast<int>(unit / wa.splits % per_adapter);
             const bool is_a = tile < wa.in_tiles;
             const int col0 = (is_a ? tile : tile - wa.in_tiles) * kWgCols;
             const int width = static_cast<int>(is_a ? g.d_in : g.d_out);
             const int z_panels = min(kWgCols / 64, (width - col0 + 63) / 64);
             int first, last;
-            const int padded = find_group(g.offsets, g.n, g.M, adapter, first, last, err);
-            for (int e0 = first; e0 < last && ok; e0 += kWgTok) {
+            const int padded = group(adapter, first, last);
+            int b0, b1;
+            share(last - first, sp, b0, b1);
+            int32_t next[4];  // the next slot's entries, loaded a slot ahead
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = first + b0 * kWgTok + (lane & 15) * 4 + i;
+                next[i] = e < last ? g.rows[e] : -1;
+            }
+            for (int e0 = first + b0 * kWgTok; e0 < min(last, first + b1 * kWgTok) && ok; e0 += kWgTok) {
                 const int count = min(kWgTok, last - e0);
                 // lane l < 16 holds entries 4 l .. 4 l + 3; rows past the last are given as M: zeros
                 int32_t row[4];
-                const int first32 =
-                    __shfl_sync(0xFFFFFFFFu, lane < 16 && 4 * lane < count ? g.rows[e0 + 4 * lane] : -1, lane & 8);
+                const int first32 = __shfl_sync(0xFFFFFFFFu, next[0], lane & 8);
                 bool follow = true;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = (lane & 15) * 4 + i;
-                    const int r = e < count ? checked_row(g.rows, e0 + e, g.M, err) : -1;
-                    follow = follow && r >= 0 && r == first32 + (e & 31);
-                    row[i] = r >= 0 ? r : static_cast<int32_t>(g.M);
+                    const bool ok_row = e < count && next[i] >= 0 && next[i] < g.M;
+                    if (e < count && !ok_row) flag_error(err, kErrIndex);
+                    follow = follow && ok_row && next[i] == first32 + (e & 31);
+                    row[i] = ok_row ? next[i] : static_cast<int32_t>(g.M);
+                    next[i] = e0 + kWgTok + e < last ? g.rows[e0 + kWgTok + e] : -1;
                 }
                 const uint32_t follows = __ballot_sync(0xFFFFFFFFu, follow || lane >= 16);
                 const bool box = ((follows >> (lane & 8)) & 0xFFu) == 0xFFu;  // 32 rows one after the other
@@ -161,10 +214,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         const uint64_t z_desc = tc::smem_desc_sw128(smem_base, kWgPanel, 1024u);
         const uint64_t t_desc = tc::smem_desc_sw128(smem_base + kWgCols / 64 * kWgPanel, kWgPanel, 1024u);
         for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
-            const int adapter = static_cast<int>(unit / per_adapter);
-            int first, last;
-            adapter_bounds(g.offsets, g.n, g.M, adapter, first, last, err);
-            if (first >= last) continue;  // no tokens: the epilogue writes zeros
+            const int adapter = static_cast<int>(unit / wa.splits / per_adapter);
+            int first, last, b0, b1;
+            group(adapter, first, last);
+            share(last - first, static_cast<int>(unit % wa.splits), b0, b1);
+            if (b0 >= b1) continue;  // no tokens: the epilogue writes zeros
+            const int e_begin = first + b0 * kWgTok, e_end = min(last, first + b1 * kWgTok);
             const bool me = tc::elect_one();
             const uint32_t i = acc & 1;
             if (me) {
@@ -172,13 +227,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 int js = s;
                 ok = tc::mbar_wait(acc_empty(i), ((acc >> 1) & 1u) ^ 1u, err);
                 const uint32_t d = tmem + i * wa.acc_cols;
-                for (int e0 = first; e0 < last && ok; e0 += kWgTok, ++jt) {
+                for (int e0 = e_begin; e0 < e_end && ok; e0 += kWgTok, ++jt) {
                     if (!(ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err))) break;
                     tc::tc_fence_after();
                     const int steps = (min(kWgTok, last - e0) + 15) / 16;
                     const uint32_t off = js * (wa.slot_bytes >> 4);
                     for (int kk = 0; kk < steps; ++kk) {
-                        const uint32_t first_step = e0 > first || kk > 0;
+                        const uint32_t first_step = e0 > e_begin || kk > 0;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint64_t zd = z_desc + off + half * (2 * kWgPanel >> 4) + kk * 128u;
@@ -193,7 +248,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 if (ok) tc::mma_commit(acc_full(i));
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1);
-            it += (last - first + kWgTok - 1) / kWgTok;
+            it += b1 - b0;
             s = it % slots;
             ++acc;
         }
@@ -207,13 +262,16 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         uint32_t acc = 0;
         bool ok = true;
         for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
-            const int adapter = static_cast<int>(unit / per_adapter), tile = static_cast<int>(unit % per_adapter);
+            const int sp = static_cast<int>(unit % wa.splits);
+            const int adapter = static_cast<int>(unit / wa.splits / per_adapter);
+            const int tile = static_cast<int>(unit / wa.splits % per_adapter);
             const bool is_a = tile < wa.in_tiles;
             const int64_t col0 = static_cast<int64_t>(is_a ? tile : tile - wa.in_tiles) * kWgCols + w4 * 32 + lane;
             const int64_t width = is_a ? g.d_in : g.d_out;
-            int first, last;
-            adapter_bounds(g.offsets, g.n, g.M, adapter, first, last, err);
-            const bool any = first < last;
+            int first, last, b0, b1;
+            group(adapter, first, last);
+            share(last - first, sp, b0, b1);
+            const bool any = b0 < b1;
             const uint32_t i = acc & 1;
             if (any) {
                 ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc_full(i), (acc >> 1) & 1u, err));
@@ -236,6 +294,19 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                     }
                     if (col >= width) {
                         // past the last column
+                    } else if (wa.splits > 1) {
+                        float* to = wa.partial + sp * wa.split_stride;
+                        if (is_a) {
+                            to += (static_cast<int64_t>(adapter) * g.rank + c0) * width + col;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c0 + j < g.rank) to[j * width] = __uint_as_float(v[j]);
+                        } else {
+                            to += wa.gb_at + (static_cast<int64_t>(adapter) * width + col) * g.rank + c0;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c0 + j < g.rank) to[j] = __uint_as_float(v[j]);
+                        }
                     } else if (is_a) {  // neighbouring lanes hold neighbouring columns
                         uint16_t* to = g.gA + (static_cast<int64_t>(adapter) * g.rank + c0) * width + col;
 #pragma unroll
@@ -277,11 +348,30 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
 }
 
+// gA and gB from the splits' sums, in order, rounded once.
+__global__ void __launch_bounds__(256) adapter_wgrad_sum_kernel(const float* partial, int64_t stride, int splits,
+                                                                uint16_t* gA, int64_t nA, uint16_t* gB, int64_t nB) {
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < nA + nB; e += static_cast<int64_t>(gridDim.x) * 256) {
+        float s = 0.f;
+        for (int k = 0; k < splits; ++k) s += partial[k * stride + e];
+        (e < nA ? gA[e] : gB[e - nA]) = float_to_bf16_bits(s);
+    }
+}
+
 }  // namespace nq
+
+// Blocks that share the tokens of a unit: as many as the multiprocessors have room for where the units
+// are few, with 512 tokens of the batch each at least.
+int nq_adapter_wgrad_splits(int64_t M, int64_t n, int64_t d_in, int64_t d_out) {
+    const int64_t units = n * ((d_in + nq::kWgCols - 1) / nq::kWgCols + (d_out + nq::kWgCols - 1) / nq::kWgCols);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({nq_host::sm_count() / units, M / 512, 8})));
+}
 
 // u_parts, t_parts: as AdapterArgs describes them (written by the transposed product's kernel).
 nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint16_t* u_parts, const uint16_t* t_parts,
-                                       int64_t part_rows, int part_ld, cudaStream_t stream, bool pdl) {
+                                       int64_t part_rows, int part_ld, float* partial, cudaStream_t stream, bool pdl) {
     nq::AdapterWgradArgs wa{};
     wa.g = g;
     wa.part_rows = part_rows;
@@ -290,8 +380,14 @@ nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint1
     wa.in_tiles = g.gA ? static_cast<int>((g.d_in + nq::kWgCols - 1) / nq::kWgCols) : 0;
     wa.out_tiles = g.gB ? static_cast<int>((g.d_out + nq::kWgCols - 1) / nq::kWgCols) : 0;
     wa.acc_cols = static_cast<uint32_t>(wa.panels) * 128u;
+    const int64_t nA = g.gA ? static_cast<int64_t>(g.n) * g.rank * g.d_in : 0;
+    const int64_t nB = g.gB ? static_cast<int64_t>(g.n) * g.rank * g.d_out : 0;
+    wa.splits = nq_adapter_wgrad_splits(g.M, g.n, g.d_in, g.d_out);
+    wa.partial = partial;
+    wa.split_stride = nA + nB;
+    wa.gb_at = nA;
     wa.slot_bytes = (nq::kWgCols / 64 + 2 * wa.panels) * nq::kWgPanel;
-    const size_t fixed = 1024 + 8 * (2 * nq::kWgMaxSlots + 5) + 8;
+    const size_t fixed = 1024 + 128 + (g.n <= nq::kWgGroups ? 12 * static_cast<size_t>(g.n) : 0);  // alignment, barriers, bounds
     constexpr size_t kSmemMax = 227 * 1024;
     wa.slots = static_cast<int>(std::min<size_t>(nq::kWgMaxSlots, (kSmemMax - fixed) / wa.slot_bytes));
     const size_t smem = fixed + wa.slots * static_cast<size_t>(wa.slot_bytes);
@@ -319,11 +415,21 @@ nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint1
             return NQ_ERR_LAUNCH;
         attr_done[dev].store(true, std::memory_order_release);
     }
-    const int64_t units = static_cast<int64_t>(wa.in_tiles + wa.out_tiles) * g.n;
+    const int64_t units = static_cast<int64_t>(wa.in_tiles + wa.out_tiles) * g.n * wa.splits;
     const int grid = static_cast<int>(std::min<int64_t>(units, nq_host::sm_count()));
     void* kargs[] = {&x64, &x32, &x1, &y64, &y32, &y1, &mu, &mt, &wa};
-    return nq_host::launch_pdl(reinterpret_cast<const void*>(nq::adapter_wgrad_umma_kernel), dim3(grid),
-                               dim3(nq::kWgThreads), smem, stream, kargs, pdl) == cudaSuccess
+    if (nq_host::launch_pdl(reinterpret_cast<const void*>(nq::adapter_wgrad_umma_kernel), dim3(grid),
+                            dim3(nq::kWgThreads), smem, stream, kargs, pdl) != cudaSuccess)
+        return NQ_ERR_LAUNCH;
+    if (wa.splits == 1) return NQ_OK;
+    const float* part = partial;
+    uint16_t *gA = g.gA, *gB = g.gB;
+    int64_t stride = wa.split_stride, nA_arg = nA, nB_arg = nB;
+    int splits = wa.splits;
+    void* sargs[] = {&part, &stride, &splits, &gA, &nA_arg, &gB, &nB_arg};
+    const int64_t blocks = std::min<int64_t>((nA + nB + 255) / 256, 8 * static_cast<int64_t>(nq_host::sm_count()));
+    return nq_host::launch_pdl(reinterpret_cast<const void*>(nq::adapter_wgrad_sum_kernel),
+                               dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, sargs, pdl) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_LAUNCH;
 }

@@ -42,7 +42,6 @@ struct AdapterUmmaArgs {
     uint32_t slot_bytes;
     int panels;   // 64-element panels of the rank
     int r16;      // rank rounded up to the MMA's K
-    int own_shift; // log2(128 / blocks of the cluster)
 };
 
 // Two bf16 values and two fp32 addends, rounded once.
@@ -54,9 +53,11 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t y, uint32_t lo, uint32_t
 // Barrier of the epilogue's warps.
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
 
-// Of `segs` segments of partial t; at least a tile of out for every warp of the epilogue.
-__host__ __device__ constexpr uint32_t inbox_bytes(int segs) {
-    return segs * kTokBytes > kEpiWarps * 4096u ? segs * kTokBytes : kEpiWarps * 4096u;
+// Of `segs` segments of partial t in a cluster of cs blocks (16 / cs groups of rows, rounded up, from each);
+// at least a tile of out for every warp of the epilogue.
+__host__ __device__ constexpr uint32_t inbox_bytes(int segs, int cs) {
+    const uint32_t t = static_cast<uint32_t>(segs * cs * ((16 + cs - 1) / cs)) * 1024u;
+    return t > kEpiWarps * 4096u ? t : kEpiWarps * 4096u;
 }
 
 template <bool BWD>
@@ -71,17 +72,19 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t smem_base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
     const int slots = ua.slots, panels = ua.panels, r16 = ua.r16;
     const uint32_t cs = cluster_nctarank(), q = cluster_ctarank();
-    const int own_shift = ua.own_shift, own_rows = 1 << own_shift;  // rows of t that a block puts together
+    // a block puts together the rows of t in groups 16 q / cs .. 16 (q + 1) / cs of 8
+    const int own_first = 16 * static_cast<int>(q) / static_cast<int>(cs);
+    const int own_groups = 16 * (static_cast<int>(q) + 1) / static_cast<int>(cs) - own_first, own_rows = 8 * own_groups;
     const uint32_t part_bytes = static_cast<uint32_t>(panels) * kTokBytes;
     const uint32_t t_base = smem_base + slots * ua.slot_bytes;  // [2 parts][panels][128 rows][128 B], swizzled
-    // Partial t of the rows that this block owns: [cs blocks][segments of 32 ranks][row groups of 32 or
-    // own_rows][8 pieces of 4 ranks][rows of the group], 16 bytes a piece.  A warp of the epilogue
-    // writes and sends what it holds of a segment and group as one run.
-    const int segs = (r16 + 31) / 32, grp_shift = min(own_shift, 5), grp = 1 << grp_shift;
-    const uint32_t seg_bytes = own_rows * 128u;
+    // Partial t of the rows that this block owns: [cs blocks][segments of 32 ranks][groups][8 pieces of 4
+    // ranks][8 rows], 16 bytes a piece.  What a warp of the epilogue holds of a segment and group, it
+    // writes and sends as one run of up to 1 KB.
+    const int segs = (r16 + 31) / 32;
+    const uint32_t seg_bytes = own_groups * 1024u;
     const uint32_t inbox = t_base + 2 * part_bytes;
     const uint32_t staging = inbox;  // between two tiles' t: the epilogue's tiles of out, 4 KB a warp
-    const uint32_t bars = inbox + inbox_bytes(segs);
+    const uint32_t bars = inbox + inbox_bytes(segs, static_cast<int>(cs));
     auto slot_at = [&](int s) { return smem_base + s * ua.slot_bytes; };
     auto full = [&](int s) { return bars + 8u * s; };
     auto free1 = [&](int s) { return bars + 8u * (kMaxSlots + s); };      // first product: its MMAs are done
@@ -132,11 +135,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
 
     const int kb_all = static_cast<int>((a.K + kStep - 1) / kStep), nb_all = static_cast<int>((a.N + kStep - 1) / kStep);
-    const int cs_shift = 7 - own_shift;  // cs = 1 << cs_shift
-    const int kb0 = static_cast<int>((static_cast<int64_t>(kb_all) * q) >> cs_shift);
-    const int kb1 = static_cast<int>((static_cast<int64_t>(kb_all) * (q + 1)) >> cs_shift);
-    const int nb0 = a.out ? static_cast<int>((static_cast<int64_t>(nb_all) * q) >> cs_shift) : 0;
-    const int nb1 = a.out ? static_cast<int>((static_cast<int64_t>(nb_all) * (q + 1)) >> cs_shift) : 0;
+    const int kb0 = kb_all * static_cast<int>(q) / static_cast<int>(cs), kb1 = kb_all * (static_cast<int>(q) + 1) / static_cast<int>(cs);
+    const int nb0 = a.out ? nb_all * static_cast<int>(q) / static_cast<int>(cs) : 0;
+    const int nb1 = a.out ? nb_all * (static_cast<int>(q) + 1) / static_cast<int>(cs) : 0;
     const uint32_t w1_bytes = BWD ? panels * 8192u : r16 * 128u;
     const uint32_t w2_bytes = BWD ? r16 * 128u : panels * 8192u;
     pdl_wait();
@@ -404,7 +405,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (ok && kb1 > kb0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc::tc_fence_after();
-            const uint32_t owner = static_cast<uint32_t>(tid >> own_shift), rl = tid & (own_rows - 1);
+            // this lane's group of 8 rows, the block that owns it and its place there
+            const int my_group = tid >> 3;
+            int owner = my_group * static_cast<int>(cs) / 16;
+            if (16 * (owner + 1) / static_cast<int>(cs) <= my_group) ++owner;
+            const int owner_first = 16 * owner / static_cast<int>(cs);
+            const uint32_t owner_bytes = (16 * (owner + 1) / static_cast<int>(cs) - owner_first) * 1024u;
+            const uint32_t at = (my_group - owner_first) * 1024u;
             for (int g = set; g < segs && ok; g += 2) {
                 uint32_t v[32];
                 if (kb1 > kb0) {
@@ -415,20 +422,22 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
                 const int pieces = min(8, (r16 - g * 32) / 4);
-                const uint32_t at = (rl >> grp_shift) * (grp * 128u);  // of the group in the segment
-                const uint32_t home = owner == q ? inbox + (q * segs + g) * seg_bytes : t_base + g * kTokBytes + owner * seg_bytes;
-                uint4* to = reinterpret_cast<uint4*>(smem_raw + (home + at - tc::smem_u32(smem_raw))) + (rl & (grp - 1));
+                // kept here for this block's own rows, else put where the owner's rows of t will arrive
+                const uint32_t home = owner == static_cast<int>(q) ? inbox + (q * segs + g) * seg_bytes + at
+                                                                    : t_base + g * kTokBytes + owner_first * 1024u + at;
+                uint4* to = reinterpret_cast<uint4*>(smem_raw + (home - tc::smem_u32(smem_raw))) + (lane & 7);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (j < pieces) to[j << grp_shift] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    if (j < pieces) to[j * 8] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                for (int o = 0; o < 32; o += grp) {
-                    const uint32_t own = __shfl_sync(0xFFFFFFFFu, owner, o), src = __shfl_sync(0xFFFFFFFFu, home + at, o);
-                    const uint32_t off = __shfl_sync(0xFFFFFFFFu, at, o);
-                    if (own != q && tc::elect_one())
-                        tc::bulk_copy_cluster(cluster_map(inbox + (q * segs + g) * seg_bytes + off, own), src,
-                                              pieces * grp * 16u, cluster_map(inbox_full, own));
+#pragma unroll
+                for (int o = 0; o < 32; o += 8) {
+                    const int own = __shfl_sync(0xFFFFFFFFu, owner, o);
+                    const uint32_t src = __shfl_sync(0xFFFFFFFFu, home, o);
+                    const uint32_t off = __shfl_sync(0xFFFFFFFFu, at + (q * segs + g) * owner_bytes, o);
+                    if (own != static_cast<int>(q) && tc::elect_one())
+                        tc::bulk_copy_cluster(cluster_map(inbox + off, own), src, pieces * 128u, cluster_map(inbox_full, own));
                     __syncwarp();
                 }
             }
@@ -444,8 +453,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             // ---- the rows this block owns
             ok = ok && tc::mbar_wait(inbox_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            for (int e = eid; e < (r16 / 8) << own_shift && ok; e += 32 * kEpiWarps) {
-                const int rr = e & (own_rows - 1), c = e >> own_shift, m = static_cast<int>(q) * own_rows + rr;
+            for (int e = eid; e < (r16 / 8) * own_rows && ok; e += 32 * kEpiWarps) {
+                const int c = e / own_rows, rr = e - c * own_rows, m = own_first * 8 + rr;
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -453,9 +462,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll 4
                     for (uint32_t src = 0; src < cs; ++src) {
                         const float4* at = reinterpret_cast<const float4*>(
-                            smem_raw + (inbox + (src * segs + c / 4) * seg_bytes + (rr >> grp_shift) * (grp * 128u) -
-                                        tc::smem_u32(smem_raw))) + (rr & (grp - 1));
-                        const float4 f0 = at[(c % 4 * 2) << grp_shift], f1 = at[(c % 4 * 2 + 1) << grp_shift];
+                            smem_raw + (inbox + (src * segs + c / 4) * seg_bytes + (rr >> 3) * 1024u -
+                                        tc::smem_u32(smem_raw))) + (rr & 7);
+                        const float4 f0 = at[c % 4 * 16], f1 = at[c % 4 * 16 + 8];
                         v[0] += f0.x;
                         v[1] += f0.y;
                         v[2] += f0.z;
@@ -515,12 +524,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (ok && eid / 32 < static_cast<int>(cs) && static_cast<uint32_t>(eid / 32) != q && tc::elect_one()) {
                 const uint32_t bar = cluster_map(t_full, eid / 32);
                 for (int g = 0; g < 2 * panels; ++g) {
-                    const uint32_t at = t_base + g * kTokBytes + q * seg_bytes;
+                    const uint32_t at = t_base + g * kTokBytes + own_first * 1024u;
                     tc::bulk_copy_cluster(cluster_map(at, eid / 32), at, seg_bytes, bar);
                 }
             }
             __syncwarp();
-            if (eid == 0) tc::mbar_arrive_expect_tx(t_full, (cs - 1) * 2 * panels * seg_bytes);
+            if (eid == 0) tc::mbar_arrive_expect_tx(t_full, (16 - own_groups) * 2 * panels * 1024u);
             // ---- out = base + the second product
             it += kb1 - kb0;
             s = it % slots;
@@ -620,8 +629,8 @@ namespace {
 
 // Clusters of cs blocks of the kernel that fit on the device at once (one block a multiprocessor).
 int resident_clusters(int dev, int cs) {
-    static std::atomic<int> known[64][4];
-    std::atomic<int>& slot = known[dev][cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0];
+    static std::atomic<int> known[64][9];
+    std::atomic<int>& slot = known[dev][cs];
     int n = slot.load(std::memory_order_acquire);
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
@@ -657,11 +666,6 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     ua.r16 = (a.rank + 15) / 16 * 16;
     ua.panels = (a.rank + 63) / 64;
     ua.slot_bytes = nq::kTokBytes + static_cast<uint32_t>(ua.panels) * 8192u;
-    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes + nq::inbox_bytes((ua.r16 + 31) / 32) +
-                         8 * (3 * nq::kMaxSlots) + 88;
-    ua.slots = static_cast<int>(std::min<size_t>(nq::kMaxSlots, (kUmmaSmemMax - fixed) / ua.slot_bytes));
-    const size_t smem = fixed + ua.slots * static_cast<size_t>(ua.slot_bytes);
-
     CUtensorMap mz, mz32, mz1, mbase, mbase32, mbase1, mout, ma, mb;
     const int box[2] = {64, nq::kTok}, box32[2] = {64, 32}, row_box[2] = {64, 1};
     const int a_box[3] = {64, ua.r16, 1}, b_box[3] = {64, 64, 1};
@@ -696,13 +700,16 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     // The tiles decide how many blocks share one: as many as a portable cluster has while every
     // tile's cluster is resident at once.  How many there are depends on the lists, which only the
     // device has: M / 128 full ones and, for every other group, one that is not.  Clusters loop
-    // over what a finer grouping adds.
+    // over what a finer grouping adds.  Above 64 ranks only powers of two leave room for three slots.
     const int64_t least = (a.M + nq::kTok - 1) / nq::kTok;
     const int64_t most = nq::max_adapter_tiles(a.M, a.n, nq::kTok, nq::kNoneTok);
     const int64_t likely = least + std::min<int64_t>(a.n, a.M) / 2;
     int cs = 8;
-    ua.own_shift = 4;
-    for (; cs > 1 && likely > resident_clusters(dev, cs); cs /= 2) ++ua.own_shift;
+    while (cs > 1 && (likely > resident_clusters(dev, cs) || (ua.panels > 1 && (cs & (cs - 1)) != 0))) --cs;
+    const size_t fixed = 1024 + 2 * static_cast<size_t>(ua.panels) * nq::kTokBytes +
+                         nq::inbox_bytes((ua.r16 + 31) / 32, cs) + 8 * (3 * nq::kMaxSlots) + 88;
+    ua.slots = static_cast<int>(std::min<size_t>(nq::kMaxSlots, (kUmmaSmemMax - fixed) / ua.slot_bytes));
+    const size_t smem = fixed + ua.slots * static_cast<size_t>(ua.slot_bytes);
     const int64_t clusters = std::min<int64_t>(most, resident_clusters(dev, cs));
     void* kargs[] = {&mz, &mz32, &mz1, &mbase, &mbase32, &mbase1, &mout, &ma, &mb, &ua};
     return nq_host::launch_ex(fn, dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(cs)),

@@ -34,7 +34,8 @@ nq_status nq_launch_adapter_rows(const nq::AdapterArgs& a, bool backward, cudaSt
 bool nq_adapter_umma_fits(const nq::AdapterArgs& a);
 nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint16_t* u_parts, const uint16_t* t_parts,
-                                       int64_t part_rows, int part_ld, cudaStream_t stream, bool pdl);
+                                       int64_t part_rows, int part_ld, float* partial, cudaStream_t stream, bool pdl);
+int nq_adapter_wgrad_splits(int64_t M, int64_t n, int64_t d_in, int64_t d_out);
 nq_status nq_launch_adapter_grad_any(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_group_rows(const int32_t* ids, int64_t M, int n, int32_t* rows, int32_t* offsets,
                                        cudaStream_t stream, bool pdl);
@@ -451,11 +452,17 @@ nq_status check_adapters(const nq_adapters* S, int64_t M) {
     return NQ_OK;
 }
 
-// Workspace of the backward pass: u [M][rank] fp32, or u and t in two bf16 parts each, in padded rows.
+// Workspace of the backward pass: u [M][rank] fp32 (CUDA cores), or u and t in two bf16 parts each, in
+// padded rows, and the sums of the blocks that share a gradient's tokens (tensor cores).
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+size_t adapter_parts_bytes(const nq_adapters* S, int64_t M) {
+    return align256(8 * static_cast<size_t>(nq::max_padded_rows(M, S->n)) * ((S->rank + 63) / 64 * 64));
+}
 size_t adapter_ws(const nq_adapters* S, int64_t M) {
-    const size_t u = static_cast<size_t>(M) * S->rank * sizeof(float);
-    const size_t parts = 8 * static_cast<size_t>(nq::max_padded_rows(M, S->n)) * ((S->rank + 63) / 64 * 64);
-    return NQ_WS_HEADER_BYTES + (std::max(u, parts) + 255) / 256 * 256;
+    const size_t u = align256(static_cast<size_t>(M) * S->rank * sizeof(float));
+    const size_t splits = nq_adapter_wgrad_splits(M, S->n, S->d_in, S->d_out);
+    const size_t sums = splits > 1 ? splits * S->n * S->rank * (S->d_in + S->d_out) * sizeof(float) : 0;
+    return NQ_WS_HEADER_BYTES + std::max(u, adapter_parts_bytes(S, M) + align256(sums));
 }
 
 nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const int32_t* offsets, int64_t M) {
@@ -476,10 +483,20 @@ nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const in
     return a;
 }
 
-bool on_tensor_cores(const nq::AdapterArgs& a) { return a.M > 16 && nq_adapter_umma_fits(a); }
+// The two products run on the tensor cores (tiles of 128 rows of an adapter) or on the CUDA cores (tiles
+// of 8).  Few rows for each loaded adapter, or (forward) few rows times rank at all, are for the
+// latter: there a tile costs little beyond reading its adapter, while the tensor cores' tile takes
+// some 20 us from start to end.  Measured at 8192 x 8192, CUDA cores and tensor cores: forward, rank
+// 16: 64 rows of 64 adapters 11 and 70 us, 64 rows of one 12 and 19, 256 of 64 24 and 69; rank 64: 4
+// rows of one 13 and 22, 64 of one 26 and 21; backward, rank 16: 64 rows of 64 10 and 71, of one 21
+// and 20; at 4096 x 4096, rank 128, 8 rows of one 20 and 17.
+bool products_on_tensor_cores(const nq::AdapterArgs& a, bool backward) {
+    const bool few = a.M <= 512 && (a.M <= 8 * static_cast<int64_t>(a.n) || (!backward && a.M * a.rank <= 1024));
+    return !(few && (a.rank <= 64 || a.M <= 4)) && nq_adapter_umma_fits(a);
+}
 
 nq_status launch_adapter(const nq::AdapterArgs& a, bool backward, cudaStream_t stream) {
-    if (on_tensor_cores(a)) return nq_launch_adapter_umma(a, backward, stream, pdl_enabled());
+    if (products_on_tensor_cores(a, backward)) return nq_launch_adapter_umma(a, backward, stream, pdl_enabled());
     return nq_launch_adapter_rows(a, backward, stream, pdl_enabled());
 }
 
@@ -540,7 +557,7 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
     a.out = xbar_out;
     a.K = S->d_out;
     a.N = S->d_in;
-    const bool tensor_cores = on_tensor_cores(a);
+    const bool tensor_cores = nq_adapter_umma_fits(a);  // for the sums over tokens
     if (tensor_cores) {
         a.part_rows = nq::max_padded_rows(M, S->n);
         a.part_ld = static_cast<int>((S->rank + 63) / 64 * 64);
@@ -571,7 +588,8 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
     g.err = nq_host::error_word();
     if (tensor_cores)
         return nq_launch_adapter_wgrad_umma(g, a.u_parts ? a.u_parts : a.t_parts, a.t_parts ? a.t_parts : a.u_parts,
-                                            a.part_rows, a.part_ld, s, pdl_enabled());
+                                            a.part_rows, a.part_ld,
+                                            reinterpret_cast<float*>(scratch + adapter_parts_bytes(S, M)), s, pdl_enabled());
     return nq_launch_adapter_grad_any(g, s, pdl_enabled());
 }
 

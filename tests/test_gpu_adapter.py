@@ -44,7 +44,10 @@ def _run(c, what=""):
 SHAPES = [(1, 64, 96, 8, 1), (1, 5, 3, 1, 1), (7, 17, 33, 3, 4), (9, 256, 264, 16, 2), (64, 512, 1000, 16, 64),
           (130, 264, 136, 24, 3), (300, 1024, 72, 128, 5), (257, 2056, 520, 40, 2), (40, 1001, 515, 20, 7),
           (3, 128, 128, 104, 300), (700, 328, 4104, 64, 3), (65, 4096, 4096, 8, 1), (200, 72, 64, 127, 2),
-          (129, 8, 8, 8, 1)]
+          (129, 8, 8, 8, 1),
+          # 17 to 150 tiles: every number of blocks that share one
+          (2100, 640, 712, 16, 1), (3000, 576, 136, 24, 2), (4100, 136, 520, 64, 2), (5000, 584, 600, 8, 1),
+          (9000, 72, 136, 40, 3), (19000, 136, 72, 16, 2), (2100, 640, 520, 128, 1)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
