@@ -509,6 +509,102 @@ __global__ void __launch_bounds__(256) adapter_grad_any_kernel(const AdapterGrad
     }
 }
 
+// Few rows an adapter: bound by writing gA and gB, 16 bytes a thread at a time, neighbouring threads side
+// by side.  A block has one adapter and either 8 ranks of 2048 columns of gA or a run of gB, and takes the tokens
+// 8 at a time.  Widths and rank in multiples of 8.
+constexpr int kSmallTokens = 8;
+constexpr int kSmallRanks = 8;    // ranks of gA of a block
+constexpr int kSmallPieces = 4;   // 16-byte pieces of gB of a thread
+
+__global__ void __launch_bounds__(256) adapter_grad_small_kernel(const AdapterGradArgs a, int a_tiles, int a_blocks) {
+    __shared__ int row[kSmallTokens];
+    __shared__ float ts[kSmallTokens][kMaxRank];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int adapter = blockIdx.y, R = a.rank, blk = blockIdx.x;
+    const bool is_a = blk < a_blocks;
+    int first, last;
+    adapter_bounds(a.offsets, a.n, a.M, adapter, first, last, a.err);
+    const float* t = is_a ? a.u : a.t;
+    auto pack = [](const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = static_cast<uint32_t>(float_to_bf16_bits(f[2 * i])) |
+                   (static_cast<uint32_t>(float_to_bf16_bits(f[2 * i + 1])) << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    // tokens e0 .. of the group: their rows and t
+    auto stage = [&](int e0) {
+        __syncthreads();
+        if (threadIdx.x < kSmallTokens)
+            row[threadIdx.x] = e0 + static_cast<int>(threadIdx.x) < last ? checked_row(a.rows, e0 + threadIdx.x, a.M, a.err)
+                                                                          : -1;
+        __syncthreads();
+        for (int e = threadIdx.x; e < kSmallTokens * R; e += 256) {
+            const int m = e / R, r = e - m * R;
+            ts[m][r] = row[m] >= 0 ? t[static_cast<int64_t>(row[m]) * R + r] : 0.f;
+        }
+        __syncthreads();
+    };
+    if (is_a) {
+        const int64_t j = (static_cast<int64_t>(blk % a_tiles) * 256 + threadIdx.x) * 8;
+        const int r0 = blk / a_tiles * kSmallRanks;
+        const bool in = j < a.d_in;
+        float acc[kSmallRanks][8];
+#pragma unroll
+        for (int r = 0; r < kSmallRanks; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[r][i] = 0.f;
+        for (int e0 = first; e0 < last; e0 += kSmallTokens) {
+            stage(e0);
+            const int count = min(kSmallTokens, last - e0);
+#pragma unroll 4
+            for (int m = 0; m < count; ++m) {
+                if (row[m] < 0 || !in) continue;
+                float x[8];
+                ld_bf16<8>(a.x + row[m] * a.d_in + j, x);
+#pragma unroll
+                for (int r = 0; r < kSmallRanks; ++r)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[r][i] = fmaf(ts[m][r0 + r], x[i], acc[r][i]);
+            }
+        }
+        if (!in) return;
+#pragma unroll
+        for (int r = 0; r < kSmallRanks; ++r)
+            *reinterpret_cast<uint4*>(a.gA + (static_cast<int64_t>(adapter) * R + r0 + r) * a.d_in + j) = pack(acc[r]);
+    } else {
+        const int per = R / 8;  // pieces of a row of gB
+        const int64_t pieces = a.d_out * per, p0 = static_cast<int64_t>(blk - a_blocks) * (256 * kSmallPieces) + threadIdx.x;
+        float acc[kSmallPieces][8];
+#pragma unroll
+        for (int k = 0; k < kSmallPieces; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[k][i] = 0.f;
+        for (int e0 = first; e0 < last; e0 += kSmallTokens) {
+            stage(e0);
+            const int count = min(kSmallTokens, last - e0);
+#pragma unroll
+            for (int k = 0; k < kSmallPieces; ++k) {
+                const int64_t p = min(p0 + k * 256, pieces - 1), i0 = p / per;
+                const int r = static_cast<int>(p - i0 * per) * 8;
+#pragma unroll 4
+                for (int m = 0; m < count; ++m) {
+                    if (row[m] < 0) continue;
+                    const float y = bf16_bits_to_float(a.ybar[row[m] * a.d_out + i0]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[k][i] = fmaf(y, ts[m][r + i], acc[k][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kSmallPieces; ++k)
+            if (p0 + k * 256 < pieces)
+                *reinterpret_cast<uint4*>(a.gB + static_cast<int64_t>(adapter) * a.d_out * R + (p0 + k * 256) * 8) = pack(acc[k]);
+    }
+}
+
 // ------------------------------------------------------------------ rows grouped by adapter
 // One warp per group (adapter, then the rows without one): it counts the rows of the groups before
 // its own, then writes its own rows in order.  No atomics: the order is that of the rows.
@@ -594,6 +690,20 @@ nq_status nq_launch_adapter_grad_any(const nq::AdapterGradArgs& a, cudaStream_t 
     return nq_host::launch_pdl(reinterpret_cast<const void*>(nq::adapter_grad_any_kernel),
                                dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.n)), dim3(256), 0, stream,
                                kargs, pdl) == cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_LAUNCH;
+}
+
+nq_status nq_launch_adapter_grad_small(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl) {
+    nq::AdapterGradArgs args = a;
+    int a_tiles = static_cast<int>((a.d_in + 2047) / 2048);
+    int a_blocks = a.gA ? a_tiles * (a.rank / nq::kSmallRanks) : 0;
+    const int64_t b_blocks =
+        a.gB ? (a.d_out * (a.rank / 8) + 256 * nq::kSmallPieces - 1) / (256 * nq::kSmallPieces) : 0;
+    void* kargs[] = {&args, &a_tiles, &a_blocks};
+    return nq_host::launch_pdl(reinterpret_cast<const void*>(nq::adapter_grad_small_kernel),
+                               dim3(static_cast<unsigned>(a_blocks + b_blocks), static_cast<unsigned>(a.n)), dim3(256), 0,
+                               stream, kargs, pdl) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_LAUNCH;
 }

@@ -36,6 +36,7 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
 nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint16_t* u_parts, const uint16_t* t_parts,
                                        int64_t part_rows, int part_ld, float* partial, cudaStream_t stream, bool pdl);
 int nq_adapter_wgrad_splits(int64_t M, int64_t n, int64_t d_in, int64_t d_out);
+nq_status nq_launch_adapter_grad_small(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_grad_any(const nq::AdapterGradArgs& a, cudaStream_t stream, bool pdl);
 nq_status nq_launch_adapter_group_rows(const int32_t* ids, int64_t M, int n, int32_t* rows, int32_t* offsets,
                                        cudaStream_t stream, bool pdl);
@@ -557,7 +558,11 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
     a.out = xbar_out;
     a.K = S->d_out;
     a.N = S->d_in;
-    const bool tensor_cores = nq_adapter_umma_fits(a);  // for the sums over tokens
+    // The sums over tokens: on the tensor cores, but for at most 8 rows for each adapter on average, where
+    // writing the gradients is all there is to it.
+    const bool vectors = S->d_in % 8 == 0 && S->d_out % 8 == 0 && S->rank % 8 == 0;
+    const bool small = vectors && M <= 512 && M <= 8 * S->n;
+    const bool tensor_cores = !small && nq_adapter_umma_fits(a);
     if (tensor_cores) {
         a.part_rows = nq::max_padded_rows(M, S->n);
         a.part_ld = static_cast<int>((S->rank + 63) / 64 * 64);
@@ -590,6 +595,7 @@ nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const i
         return nq_launch_adapter_wgrad_umma(g, a.u_parts ? a.u_parts : a.t_parts, a.t_parts ? a.t_parts : a.u_parts,
                                             a.part_rows, a.part_ld,
                                             reinterpret_cast<float*>(scratch + adapter_parts_bytes(S, M)), s, pdl_enabled());
+    if (small) return nq_launch_adapter_grad_small(g, s, pdl_enabled());
     return nq_launch_adapter_grad_any(g, s, pdl_enabled());
 }
 

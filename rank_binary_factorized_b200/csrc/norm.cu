@@ -842,25 +842,27 @@ __global__ void __launch_bounds__(512, 1) block_norm_grad_rows_kernel(const Norm
     }
 }
 
-// out[k][i] = sum over the blocks' partial sums, in fp64: 8 threads a column, each with every eighth
-// block, then the 8 in order.
-__global__ void __launch_bounds__(256) norm_vector_sums_kernel(const NormSumArgs a) {
-    __shared__ double part[8][32];
+// out[k][i] = sum over the blocks' partial sums, in fp64: 32 threads a column, each with every 32nd
+// block, then the 32 in order.
+__global__ void __launch_bounds__(1024) norm_vector_sums_kernel(const NormSumArgs a) {
+    __shared__ double part[32][33];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
-    const int k = blockIdx.y, g = threadIdx.x >> 5;
-    if (!a.out[k]) return;
+    const int g = threadIdx.x >> 5;
+    const float* from = a.part[blockIdx.y];
+    float* out = a.out[blockIdx.y];
+    if (!out) return;
     double s = 0.0;
     if (i < a.d) {
-#pragma unroll 8
-        for (int b = g; b < a.blocks; b += 8) s += static_cast<double>(a.part[k][static_cast<int64_t>(b) * a.d + i]);
+#pragma unroll 4
+        for (int b = g; b < a.blocks; b += 32) s += static_cast<double>(from[static_cast<int64_t>(b) * a.d + i]);
     }
     part[g][threadIdx.x & 31] = s;
     __syncthreads();
     if (g == 0 && i < a.d) {
-        for (int j = 1; j < 8; ++j) s += part[j][threadIdx.x];
-        a.out[k][i] = static_cast<float>(s);
+        for (int j = 1; j < 32; ++j) s += part[j][threadIdx.x];
+        out[i] = static_cast<float>(s);
     }
 }
 
@@ -881,7 +883,9 @@ int ring_blocks_per_sm(int64_t d) { return std::max(1, std::min(16, 512 / row_th
 // Backward: blocks that share the rows; rows too wide for the ring take two blocks of any size.
 int grad_blocks(int64_t d, int64_t M) {
     const int per_sm = d <= kRingMaxD ? ring_blocks_per_sm(d) : 2;
-    return static_cast<int>(std::min<int64_t>(M, static_cast<int64_t>(per_sm) * nq_host::sm_count()));
+    // narrow rows: some for each block, so that the blocks' sums stay small beside the rows
+    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(16, 4096 / d));
+    return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, static_cast<int64_t>(per_sm) * nq_host::sm_count()));
 }
 
 // Lays out the stages: a row that does not start on 16 bytes brings up to 15 before and after it, and
@@ -1014,5 +1018,5 @@ nq_status nq_launch_block_norm_grad(const nq::NormBwdArgs& a, float* g_w_pre, fl
     if (st != NQ_OK || !any) return st;
     void* sargs[] = {&sum};
     return launched(nq_host::launch_pdl(reinterpret_cast<const void*>(nq::norm_vector_sums_kernel),
-                                        dim3(static_cast<unsigned>((a.d + 31) / 32), 3), dim3(256), 0, stream, sargs, pdl));
+                                        dim3(static_cast<unsigned>((a.d + 31) / 32), 3), dim3(1024), 0, stream, sargs, pdl));
 }
