@@ -361,20 +361,20 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_any_kernel(const Norm
     }
 }
 
-// Blocks take rows in turn; block b keeps its sums over rows for the vectors' gradients in
-// part[k][b][d] (k = g_w_pre, g_w_post, g_gate), each column always by the same thread.
+// Blocks take rows in turn; block b keeps its sums over rows in part[k][b][.], each column always by
+// the same thread.
 __global__ void __launch_bounds__(kNormThreads) block_norm_grad_any_kernel(const NormBwdArgs a) {
     __shared__ float red[96];
     pdl_wait();
     pdl_launch_dependents();
     const float inv_d = 1.0f / static_cast<float>(a.d);
     const bool row_gate = a.gate && a.ld_gate > 0;
-    float* part[3];
-    for (int k = 0; k < 3; ++k)
-        part[k] = a.part[k] ? a.part[k] + static_cast<int64_t>(blockIdx.x) * a.d : nullptr;
-    for (int k = 0; k < 3; ++k)
-        if (part[k])
-            for (int64_t i = threadIdx.x; i < a.d; i += kNormThreads) part[k][i] = 0.f;
+    float* const part0 = a.part[0] ? a.part[0] + static_cast<int64_t>(blockIdx.x) * a.part_ld : nullptr;
+    float* const part1 = a.part[1] ? a.part[1] + static_cast<int64_t>(blockIdx.x) * a.part_ld : nullptr;
+    for (int64_t i = threadIdx.x; i < a.d; i += kNormThreads) {
+        if (part0) part0[i] = 0.f;
+        if (part1) part1[i] = 0.f;
+    }
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
         const int64_t base = m * a.d;
         const uint16_t* gate = a.gate ? a.gate + m * a.ld_gate : nullptr;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_grad_any_kernel(const
         block_sum(s, red);
         const float r = rsqrtf(s[0] * inv_d + a.eps);
         const float c = s[1] * inv_d * r * r;  // mean(w gx h^) / q(h'), for h^ = h' r
-        const float rp = rsqrtf(s[2] * inv_d + a.eps);
+        const float rp = a.post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
         auto dh_of = [&](int64_t i, float hn) {  // hn = h'^
             float g = a.gh_out ? ld_h(a.gh_out, base + i, a.h_f32) : 0.f;
             if (a.gx) g += r * ld_w(a.w_pre, i, a.w_offset) * bf16_bits_to_float(a.gx[base + i]) - hn * c;
@@ -411,14 +411,13 @@ __global__ void __launch_bounds__(kNormThreads) block_norm_grad_any_kernel(const
         for (int64_t i = threadIdx.x; i < a.d; i += kNormThreads) {
             const float hn = ld_h(a.h_out, base + i, a.h_f32) * r;
             const float dh = dh_of(i, hn);
-            if (part[0] && a.gx) part[0][i] += bf16_bits_to_float(a.gx[base + i]) * hn;
+            if (part0 && a.gx) part0[i] += bf16_bits_to_float(a.gx[base + i]) * hn;
             if (a.y) {
                 const float gt = gate ? bf16_bits_to_float(gate[i]) : 1.f;
                 const float y = bf16_bits_to_float(a.y[base + i]);
                 const float w = ld_w(a.w_post, i, a.w_offset);
                 const float yn = y * rp, z = a.post ? yn * w : y, dz = dh * gt;
-                if (part[1]) part[1][i] += dz * yn;
-                if (part[2]) part[2][i] += dh * z;
+                if (part1) part1[i] += (row_gate ? dz : dh) * yn;
                 if (row_gate && a.g_gate_rows) a.g_gate_rows[base + i] = float_to_bf16_bits(dh * z);
                 if (a.gy) a.gy[base + i] = float_to_bf16_bits(a.post ? rp * (w * dz - yn * cp) : dz);
             }
@@ -815,54 +814,63 @@ __global__ void __launch_bounds__(512, 1) block_norm_grad_rows_kernel(const Norm
         }
         if (++s == ring.stages) s = 0;
     }
-    // g_w_pre; g_w_post = gate sum dh' y^; g_gate = w_post' sum dh' y^
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-        const int c = col_of(k);
-        float g[8], w[8], v0[8], v1[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v0[2 * i] = lo_of(acc0[k][i]);
-            v0[2 * i + 1] = hi_of(acc0[k][i]);
-            v1[2 * i] = lo_of(acc1[k][i]);
-            v1[2 * i + 1] = hi_of(acc1[k][i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = 1.f;
-        if (!ROWGATE && a.gate) load8_vector(a.gate, c, d, g);
-        weight8(a.post ? a.w_post : nullptr, a.w_offset, c, d, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c + i >= d) continue;
-            const int64_t at = static_cast<int64_t>(blockIdx.x) * a.d + c + i;
-            if (a.part[0]) a.part[0][at] = v0[i];
-            if (a.part[1]) a.part[1][at] = g[i] * v1[i];
-            if (a.part[2]) a.part[2][at] = w[i] * v1[i];
-        }
+        if (col_of(k) >= d) continue;
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * a.part_ld + col_of(k);  // part_ld: a multiple of 8
+        auto put = [&](float* part, const F2 (&v)[4]) {
+            float4* to = reinterpret_cast<float4*>(part + at);
+            to[0] = make_float4(lo_of(v[0]), hi_of(v[0]), lo_of(v[1]), hi_of(v[1]));
+            to[1] = make_float4(lo_of(v[2]), hi_of(v[2]), lo_of(v[3]), hi_of(v[3]));
+        };
+        if (a.part[0]) put(a.part[0], acc0[k]);
+        if (a.part[1]) put(a.part[1], acc1[k]);
     }
 }
 
-// out[k][i] = sum over the blocks' partial sums, in fp64: 32 threads a column, each with every 32nd
-// block, then the 32 in order.
-__global__ void __launch_bounds__(1024) norm_vector_sums_kernel(const NormSumArgs a) {
-    __shared__ double part[32][33];
+// The vectors' gradients from the blocks' sums: a block of W warps has 32 C columns (C a lane), a warp
+// every W-th block's sums of them, added up in fp64; then the W in order.  Narrow rows come from more
+// blocks and have fewer columns: there C = 1 and W = 32 keep more loads in flight.
+template <int C, int W>
+__global__ void __launch_bounds__(32 * W) norm_vector_sums_kernel(const NormSumArgs a) {
+    __shared__ double part[W][32 * C];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
-    const int g = threadIdx.x >> 5;
-    const float* from = a.part[blockIdx.y];
-    float* out = a.out[blockIdx.y];
-    if (!out) return;
-    double s = 0.0;
-    if (i < a.d) {
-#pragma unroll 4
-        for (int b = g; b < a.blocks; b += 32) s += static_cast<double>(from[static_cast<int64_t>(b) * a.d + i]);
+    const bool second = blockIdx.y != 0;
+    const float* from = second ? a.part[1] : a.part[0];
+    if (!from) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * (32 * C) + lane * C;
+    double s[C] = {};
+    if (c < a.part_ld) {
+#pragma unroll 8
+        for (int b = warp; b < a.blocks; b += W) {
+            const float* p = from + b * a.part_ld + c;
+            if constexpr (C == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p);
+                s[0] += v.x;
+                s[1] += v.y;
+                s[2] += v.z;
+                s[3] += v.w;
+            } else {
+                s[0] += *p;
+            }
+        }
     }
-    part[g][threadIdx.x & 31] = s;
+#pragma unroll
+    for (int i = 0; i < C; ++i) part[warp][lane * C + i] = s[i];
     __syncthreads();
-    if (g == 0 && i < a.d) {
-        for (int j = 1; j < 32; ++j) s += part[j][threadIdx.x];
-        out[i] = static_cast<float>(s);
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (32 * C) + threadIdx.x;
+    if (threadIdx.x >= 32 * C || i >= a.d) return;
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += part[w][threadIdx.x];
+    const float v = static_cast<float>(sum);
+    if (!second) {
+        a.g_w_pre[i] = v;
+    } else {
+        if (a.g_w_post) a.g_w_post[i] = a.gate ? static_cast<float>(sum * bf16_bits_to_float(a.gate[i])) : v;
+        if (a.g_gate) a.g_gate[i] = a.w_post ? static_cast<float>(sum * (a.w_offset + bf16_bits_to_float(a.w_post[i]))) : v;
     }
 }
 
@@ -884,7 +892,7 @@ int ring_blocks_per_sm(int64_t d) { return std::max(1, std::min(16, 512 / row_th
 int grad_blocks(int64_t d, int64_t M) {
     const int per_sm = d <= kRingMaxD ? ring_blocks_per_sm(d) : 2;
     // narrow rows: some for each block, so that the blocks' sums stay small beside the rows
-    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(16, 4096 / d));
+    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(4, 2048 / d));
     return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, static_cast<int64_t>(per_sm) * nq_host::sm_count()));
 }
 
@@ -978,27 +986,19 @@ nq_status nq_launch_block_norm(const nq::NormFwdArgs& a, int64_t M, cudaStream_t
 }
 
 size_t nq_block_norm_grad_ws(int64_t d, int64_t M) {
-    return NQ_WS_HEADER_BYTES + 3 * static_cast<size_t>(grad_blocks(d, M)) * d * sizeof(float);
+    return NQ_WS_HEADER_BYTES + 2 * static_cast<size_t>(grad_blocks(d, M)) * ((d + 7) / 8 * 8) * sizeof(float);
 }
 
 nq_status nq_launch_block_norm_grad(const nq::NormBwdArgs& a, float* g_w_pre, float* g_w_post, float* g_gate, void* ws,
                                     cudaStream_t stream, bool pdl) {
     const int blocks = grad_blocks(a.d, a.M);
+    const bool row_gate = a.gate && a.ld_gate > 0;
     nq::NormBwdArgs args = a;
     args.err = nq_host::error_word();
-    nq::NormSumArgs sum{};
-    float* out[3] = {g_w_pre, g_w_post, g_gate};
+    args.part_ld = (a.d + 7) / 8 * 8;
     float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + NQ_WS_HEADER_BYTES);
-    bool any = false;
-    for (int k = 0; k < 3; ++k) {
-        args.part[k] = out[k] ? p + static_cast<int64_t>(k) * blocks * a.d : nullptr;
-        sum.part[k] = args.part[k];
-        sum.out[k] = out[k];
-        any = any || out[k];
-    }
-    sum.d = a.d;
-    sum.blocks = blocks;
-    const bool row_gate = a.gate && a.ld_gate > 0;
+    args.part[0] = g_w_pre ? p : nullptr;
+    args.part[1] = g_w_post || g_gate ? p + static_cast<int64_t>(blocks) * args.part_ld : nullptr;
     nq::NormRing ring{};
     ring.s16[0] = a.y;
     ring.s16[1] = a.gx;
@@ -1015,8 +1015,24 @@ nq_status nq_launch_block_norm_grad(const nq::NormBwdArgs& a, float* g_w_pre, fl
     }
     void* kargs[] = {&args, &ring};
     nq_status st = launched(nq_host::launch_pdl(fn, dim3(blocks), dim3(threads), smem, stream, kargs, pdl));
-    if (st != NQ_OK || !any) return st;
+    if (st != NQ_OK || !(args.part[0] || args.part[1])) return st;
+    nq::NormSumArgs sum{};
+    sum.part[0] = args.part[0];
+    sum.part[1] = args.part[1];
+    sum.part_ld = args.part_ld;
+    sum.d = a.d;
+    sum.blocks = blocks;
+    sum.gate = row_gate ? nullptr : a.gate;
+    sum.w_post = a.post ? a.w_post : nullptr;
+    sum.w_offset = a.w_offset;
+    sum.g_w_pre = g_w_pre;
+    sum.g_w_post = g_w_post;
+    sum.g_gate = g_gate;
     void* sargs[] = {&sum};
-    return launched(nq_host::launch_pdl(reinterpret_cast<const void*>(nq::norm_vector_sums_kernel),
-                                        dim3(static_cast<unsigned>((a.d + 31) / 32), 3), dim3(1024), 0, stream, sargs, pdl));
+    const bool narrow = a.d <= 2048;
+    const void* sums = narrow ? reinterpret_cast<const void*>(nq::norm_vector_sums_kernel<1, 32>)
+                              : reinterpret_cast<const void*>(nq::norm_vector_sums_kernel<4, 16>);
+    const int64_t cols = narrow ? 32 : 128;
+    return launched(nq_host::launch_pdl(sums, dim3(static_cast<unsigned>((a.d + cols - 1) / cols), 2),
+                                        dim3(narrow ? 1024 : 512), 0, stream, sargs, pdl));
 }

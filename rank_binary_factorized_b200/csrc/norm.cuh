@@ -32,7 +32,9 @@ struct NormBwdArgs {
     void* gh;               // outputs, each may be nullptr
     uint16_t* gy;
     uint16_t* g_gate_rows;  // [M][d] bf16, for a gate per row
-    float* part[3];         // [blocks][d] sums over a block's rows: g_w_pre, g_w_post, g_gate
+    // [blocks][part_ld] sums over a block's rows, or nullptr: gx h'^, and dh' y^ (times a gate per row)
+    float* part[2];
+    int64_t part_ld;
     int64_t M, d, ld_gate;
     float alpha, eps, w_offset;
     bool post, h_f32;
@@ -40,10 +42,13 @@ struct NormBwdArgs {
 };
 
 struct NormSumArgs {
-    const float* part[3];
-    float* out[3];
-    int64_t d;
+    const float* part[2];
+    int64_t part_ld, d;
     int blocks;
+    const uint16_t* gate;    // shared gate or nullptr (ones): g_w_post = gate sum dh' y^
+    const uint16_t* w_post;  // nullptr (ones): g_gate = (w_offset + w_post) sum dh' y^
+    float w_offset;
+    float *g_w_pre, *g_w_post, *g_gate;  // each may be nullptr
 };
 
 }  // namespace nq
