@@ -55,8 +55,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto acc_empty = [&](int i) { return bars + 8u * (2 * kWgMaxSlots + 2 + i); };
     const uint32_t drain = bars + 8u * (2 * kWgMaxSlots + 4), tmem_slot = drain + 8u;
     // bounds of every adapter's rows (where there are not too many): first, last, first padded row
-    int(*const bounds)[3] = reinterpret_cast<int(*)[3]>(smem_raw + (bars + 128u - tc::smem_u32(smem_raw)));
-    const bool kept = g.n <= kWgGroups;
+    int(*const bounds)[3] = reinterpret_cast<int(*)[3]>(smem_raw + (bars + 384u - tc::smem_u32(smem_raw)));
+    const bool kept = g.n <= kWgGroups, sorted = g.n <= 64;
+    int* const order = reinterpret_cast<int*>(smem_raw + (bars + 128u - tc::smem_u32(smem_raw)));  // of 64 at most
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int* err = g.err;
 
@@ -111,9 +112,29 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 }
                 padded += __shfl_sync(0xFFFFFFFFu, upto, 31);
             }
+            __syncwarp();
+            // adapters by their number of rows, most first (equal ones by index)
+            for (int i = lane; i < g.n && sorted; i += 32) {
+                const int mine = bounds[i][1] - bounds[i][0];
+                int place = 0;
+                for (int j = 0; j < g.n; ++j) {
+                    const int other = bounds[j][1] - bounds[j][0];
+                    place += other > mine || (other == mine && j < i);
+                }
+                order[place] = i;
+            }
         }
         __syncthreads();
     }
+    // The blocks take units in turn, there and back, from the longest adapter's on: a block's last unit is
+    // short where its others were long.
+    auto unit_of = [&](int64_t round) {
+        return round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    };
+    auto adapter_of = [&](int64_t unit) {
+        const int a = static_cast<int>(unit / wa.splits / per_adapter);
+        return sorted ? order[a] : a;
+    };
     auto group = [&](int adapter, int& first, int& last) {  // returns the first padded row (warp-wide)
         if (!kept) return find_group(g.offsets, g.n, g.M, adapter, first, last, err);
         first = bounds[adapter][0];
@@ -126,9 +147,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         uint32_t it = 0;
         int s = 0;
         bool ok = true;
-        for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
+        for (int64_t round = 0, unit; (unit = unit_of(round)) < units && ok; ++round) {
             const int sp = static_cast<int>(unit % wa.splits);
-            const int adapter = static_cast<int>(unit / wa.splits / per_adapter);
+            const int adapter = adapter_of(unit);
             const int tile = static_cast<int>(unit / wa.splits % per_adapter);
             const bool is_a = tile < wa.in_tiles;
             const int col0 = (is_a ? tile : tile - wa.in_tiles) * kWgCols;
@@ -213,8 +234,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         bool ok = true;
         const uint64_t z_desc = tc::smem_desc_sw128(smem_base, kWgPanel, 1024u);
         const uint64_t t_desc = tc::smem_desc_sw128(smem_base + kWgCols / 64 * kWgPanel, kWgPanel, 1024u);
-        for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
-            const int adapter = static_cast<int>(unit / wa.splits / per_adapter);
+        for (int64_t round = 0, unit; (unit = unit_of(round)) < units && ok; ++round) {
+            const int adapter = adapter_of(unit);
             int first, last, b0, b1;
             group(adapter, first, last);
             share(last - first, static_cast<int>(unit % wa.splits), b0, b1);
@@ -261,9 +282,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         const int w4 = warp & 3;
         uint32_t acc = 0;
         bool ok = true;
-        for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
+        for (int64_t round = 0, unit; (unit = unit_of(round)) < units && ok; ++round) {
             const int sp = static_cast<int>(unit % wa.splits);
-            const int adapter = static_cast<int>(unit / wa.splits / per_adapter);
+            const int adapter = adapter_of(unit);
             const int tile = static_cast<int>(unit / wa.splits % per_adapter);
             const bool is_a = tile < wa.in_tiles;
             const int64_t col0 = static_cast<int64_t>(is_a ? tile : tile - wa.in_tiles) * kWgCols + w4 * 32 + lane;
@@ -387,7 +408,7 @@ nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint1
     wa.split_stride = nA + nB;
     wa.gb_at = nA;
     wa.slot_bytes = (nq::kWgCols / 64 + 2 * wa.panels) * nq::kWgPanel;
-    const size_t fixed = 1024 + 128 + (g.n <= nq::kWgGroups ? 12 * static_cast<size_t>(g.n) : 0);  // alignment, barriers, bounds
+    const size_t fixed = 1024 + 384 + (g.n <= nq::kWgGroups ? 12 * static_cast<size_t>(g.n) : 0);  // alignment, barriers and order, bounds
     constexpr size_t kSmemMax = 227 * 1024;
     wa.slots = static_cast<int>(std::min<size_t>(nq::kWgMaxSlots, (kSmemMax - fixed) / wa.slot_bytes));
     const size_t smem = fixed + wa.slots * static_cast<size_t>(wa.slot_bytes);

@@ -552,6 +552,27 @@ def _rows_ptr(t, name: str, dtype, M: int, cols: int, device) -> int:
     return t.data_ptr()
 
 
+def _array_ptr(t, name: str, dtype, shape, device) -> int:
+    """The same for any shape."""
+    try:
+        if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape=shape, device=device)
+    return t.data_ptr()
+
+
+def _ws_ptr(ws, device) -> int:
+    try:
+        if ws.dtype is torch.uint8 and ws.device == device and ws.is_contiguous():
+            return ws.data_ptr()
+    except AttributeError:
+        pass
+    _need_ws(ws, device)
+    return ws.data_ptr()
+
+
 def _check_groups(ad: Adapters, groups: AdapterRows) -> None:
     if groups.n != ad.n or groups.rows.device != ad.device:
         raise ValueError("groups: for %d adapters on %s, the call has %d on %s" %
@@ -601,16 +622,15 @@ def adapter_backward(ad: Adapters, groups: AdapterRows, x, ybar: torch.Tensor, t
             gA = torch.empty((ad.n, ad.rank, ad.d_in), dtype=_BF16, device=dev)
         if gB is None:
             gB = torch.empty((ad.n, ad.d_out, ad.rank), dtype=_BF16, device=dev)
-        _need(gA, "gA", _BF16, shape=(ad.n, ad.rank, ad.d_in), device=dev)
-        _need(gB, "gB", _BF16, shape=(ad.n, ad.d_out, ad.rank), device=dev)
-        pa, pb = gA.data_ptr(), gB.data_ptr()
+        pa = _array_ptr(gA, "gA", _BF16, (ad.n, ad.rank, ad.d_in), dev)
+        pb = _array_ptr(gB, "gB", _BF16, (ad.n, ad.d_out, ad.rank), dev)
     else:
         gA = gB = None
     if ws is None:
         ws = ad.workspace(M)
-    _need_ws(ws, dev)
+    pw = _ws_ptr(ws, dev)
     _call("nq_adapter_backward", _lib.nq_adapter_backward, dev, stream, ad._ref, groups._rows_ptr, groups._offsets_ptr,
-          px, pyb, pt, pxb, po, pa, pb, M, ws.data_ptr(), ws.numel())
+          px, pyb, pt, pxb, po, pa, pb, M, pw, ws.numel())
     return out, gA, gB
 
 
@@ -682,8 +702,7 @@ def _check_gate(norm: BlockNorm, gate, M: int, device):
             raise ValueError("gate: expected [%d] or [%d][%d], got shape %s strides %s" %
                              (norm.d, M, norm.d, tuple(gate.shape), tuple(gate.stride())))
         return gate.data_ptr(), max(int(gate.stride(0)), norm.d)
-    _need(gate, "gate", _BF16, shape=(norm.d,), device=device)
-    return gate.data_ptr(), 0
+    return _array_ptr(gate, "gate", _BF16, (norm.d,), device), 0
 
 
 def block_norm(norm: BlockNorm, y, h: torch.Tensor, gate=None, h_out=None, x=None, stream=None):
@@ -724,8 +743,7 @@ def block_norm_backward(norm: BlockNorm, y, h_out: torch.Tensor, gx, gh_out, gat
             return None, 0
         if v is None:
             v = torch.empty(d, dtype=torch.float32, device=dev)
-        _need(v, name, torch.float32, shape=(d,), device=dev)
-        return v, v.data_ptr()
+        return v, _array_ptr(v, name, torch.float32, (d,), dev)
 
     def rows(v, name, dtype):
         if v is None:
@@ -745,9 +763,9 @@ def block_norm_backward(norm: BlockNorm, y, h_out: torch.Tensor, gx, gh_out, gat
         g_gate, pgg = rows(g_gate, "g_gate", _BF16)
     if ws is None:
         ws = norm.workspace(M, dev)
-    _need_ws(ws, dev)
+    pw = _ws_ptr(ws, dev)
     _call("nq_block_norm_backward", _lib.nq_block_norm_backward, dev, stream, params, py, h_out.data_ptr(), pg, ldg, pgx,
-          pgo, pgh, pgy, pwp, pwo, pgg, M, ws.data_ptr(), ws.numel())
+          pgo, pgh, pgy, pwp, pwo, pgg, M, pw, ws.numel())
     return gh, gy, g_w_pre, g_w_post, g_gate
 
 
