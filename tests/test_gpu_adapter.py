@@ -8,7 +8,7 @@ from tests.operator_util import adapter_grad_reference, adapter_reference, check
 pytestmark = pytest.mark.gpu
 
 
-def _make(M, d_in, d_out, rank, n, ids=None, seed=0, pad=0, scale=True):
+def _make(M, d_in, d_out, rank, n, ids=None, seed=0, pad=0, pad_b=None, scale=True):
     g = torch.Generator(device="cuda").manual_seed(seed + 31 * M + d_in)
 
     def rnd(*shape, std=1.0):
@@ -16,7 +16,9 @@ def _make(M, d_in, d_out, rank, n, ids=None, seed=0, pad=0, scale=True):
 
     if ids is None:
         ids = torch.randint(-1, n, (M,), generator=g, device="cuda", dtype=torch.int32)
-    A, B = rnd(n, rank, d_in + pad, std=d_in ** -0.5)[..., :d_in], rnd(n, d_out, rank + pad, std=rank ** -0.5)[..., :rank]
+    pad_b = pad if pad_b is None else pad_b
+    A = rnd(n, rank, d_in + pad, std=d_in ** -0.5)[..., :d_in]
+    B = rnd(n, d_out, rank + pad_b, std=rank ** -0.5)[..., :rank]
     s = torch.rand(n, generator=g, device="cuda") + 0.5 if scale else None
     return dict(ids=ids, A=A, B=B, scale=s, x=rnd(M, d_in), y=rnd(M, d_out), ybar=rnd(M, d_out, std=0.1),
                 xbar=rnd(M, d_in, std=0.1))
@@ -73,6 +75,75 @@ def test_adapter_groupings(M, d_in, d_out, rank):
 def test_adapter_strides_and_unit_scale(M, pad, scale):
     need_gpu()
     _run(_make(M, 256, 320, 16, 3, pad=pad, scale=scale), "pad %d" % pad)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("rank,pad_b", [(13, 3), (3, 5), (121, 7), (65, 7)])
+def test_adapter_odd_ranks_with_rows_on_16_bytes(M, rank, pad_b):
+    need_gpu()
+    _run(_make(M, 200, 328, rank, 2, pad=8, pad_b=pad_b), "rank %d" % rank)
+
+
+def test_adapter_rows_in_any_order():
+    """A caller's own lists: the rows of a group need not be in order or side by side."""
+    need_gpu()
+    for M, n, d in ((20, 2, 64), (700, 3, 136), (700, 3, 139)):
+        c = _make(M, d, d, 16, n)
+        ad, groups, t, out, back = _run(c)
+        order = torch.randperm(M, device="cuda")
+        key = torch.where(c["ids"] < 0, n, c["ids"]).long()[order]
+        rows = order[torch.sort(key, stable=True).indices].int()
+        mine = nq().AdapterRows(rows, groups.offsets)
+        t2 = torch.empty_like(t)
+        assert torch.equal(nq().adapter_forward(ad, mine, c["x"], c["y"], t=t2), out) and torch.equal(t, t2)
+        got = nq().adapter_backward(ad, mine, c["x"], c["ybar"], t, c["xbar"])
+        assert torch.equal(got[0], back[0])
+        refs, tols = adapter_grad_reference(c["A"], c["B"], c["scale"], c["ids"], c["x"], c["ybar"], t, c["xbar"])
+        for g, r, e in zip(got, refs, tols):
+            check(g, r, e, "rows in any order")
+        nq().sync_status()
+
+
+def test_adapter_first_call_of_a_process_inside_a_capture():
+    """Nothing that a call sets up on its first use needs a call outside a capture before it."""
+    need_gpu()
+    code = """
+import torch
+from rank_binary_factorized_b200 import nq
+torch.manual_seed(0)
+for M in (3, 300):
+    A, B = torch.randn(2, 16, 256, device="cuda").bfloat16(), torch.randn(2, 264, 16, device="cuda").bfloat16()
+    x, y = torch.randn(M, 256, device="cuda").bfloat16(), torch.randn(M, 264, device="cuda").bfloat16()
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) % 2
+    ad, t = nq.Adapters(A, B), torch.empty(M, 16, device="cuda")
+    N = nq.BlockNorm(256, w_pre=x[0].clone())
+    ws, wn = ad.workspace(M), N.workspace(M)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gr = nq.adapter_rows(ids, 2)
+        out = nq.adapter_forward(ad, gr, x, y, t=t)
+        back = nq.adapter_backward(ad, gr, x, y, t, x, ws=ws)
+        norm = nq.block_norm(N, None, x)
+        nback = nq.block_norm_backward(N, None, x, x, None, ws=wn)
+    g.replay()
+    torch.cuda.synchronize()
+    kept = [v.clone() for v in (out, t) + back + norm + (nback[0], nback[2])]
+    gr = nq.adapter_rows(ids, 2)
+    t2 = torch.empty_like(t)
+    want = [nq.adapter_forward(ad, gr, x, y, t=t2), t2] + list(nq.adapter_backward(ad, gr, x, y, t2, x))
+    want += list(nq.block_norm(N, None, x))
+    nb = nq.block_norm_backward(N, None, x, x, None)
+    want += [nb[0], nb[2]]
+    nq.sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(kept, want))
+print("same")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
 
 
 def test_adapter_rows_are_grouped_in_order():

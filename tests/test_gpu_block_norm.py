@@ -57,6 +57,13 @@ def test_norm_wide_and_long(M, d, f32):
     _both(_make(M, d, f32, "channel", 11 + M), True, what="M=%d d=%d" % (M, d))
 
 
+@pytest.mark.parametrize("f32,gate", [(False, "row"), (True, "channel")])
+@pytest.mark.parametrize("M,d", [(5000, 1), (3001, 3), (1500, 9), (2000, 31), (400, 255), (1000, 513), (297, 8191)])
+def test_norm_many_narrow_rows(M, d, f32, gate):
+    need_gpu()
+    _both(_make(M, d, f32, gate, M + d), True, what="M=%d d=%d" % (M, d))
+
+
 def test_norm_without_a_block():
     need_gpu()
     c = _make(9, 1024, False, None, 5, with_y=False)
