@@ -403,14 +403,16 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
 #pragma unroll
                     for (int m = 0; m < NT; ++m) {
                         if (m < count && s.row[m] >= 0) {
-                            alignas(16) uint16_t now[V];
-#pragma unroll
-                            for (int i = 0; i < V; ++i) now[i] = float_to_bf16_bits(bf16_bits_to_float(old[m][i]) + acc[m][i]);
                             uint16_t* to = a.out + s.row[m] * a.N + j;
+                            float now[V];
+#pragma unroll
+                            for (int i = 0; i < V; ++i) now[i] = bf16_bits_to_float(old[m][i]) + acc[m][i];
                             if constexpr (V == 8)
-                                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(now);
+                                *reinterpret_cast<uint4*>(to) =
+                                    make_uint4(pack_bf16(now[0], now[1]), pack_bf16(now[2], now[3]),
+                                               pack_bf16(now[4], now[5]), pack_bf16(now[6], now[7]));
                             else
-                                *to = now[0];
+                                *to = float_to_bf16_bits(now[0]);
                         }
                     }
                 }
@@ -530,8 +532,7 @@ __global__ void __launch_bounds__(256) adapter_grad_small_kernel(const AdapterGr
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = static_cast<uint32_t>(float_to_bf16_bits(f[2 * i])) |
-                   (static_cast<uint32_t>(float_to_bf16_bits(f[2 * i + 1])) << 16);
+            w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
     // tokens e0 .. of the group: their rows and t

@@ -6,10 +6,6 @@
 
 namespace nq {
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
-}
-
 // What v's bf16 part leaves of it (nothing of an infinity).
 __device__ __forceinline__ float rest_of(float v, uint32_t part) {
     const float p = __uint_as_float(part);

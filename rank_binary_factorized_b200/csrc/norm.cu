@@ -66,9 +66,6 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* red) {
 __device__ __forceinline__ int col_of(int k) {
     return (k * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
-}
 __device__ __forceinline__ void unpack8(const uint32_t (&a)[4], float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -174,7 +171,7 @@ template <bool SHIFT>
 __device__ __forceinline__ void store8(uint16_t* row, int c, int d, const float (&v)[8]) {
     uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pack2(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) p[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     if constexpr (!SHIFT) {
         if (c < d) *reinterpret_cast<uint4*>(row + c) = make_uint4(p[0], p[1], p[2], p[3]);
     } else {

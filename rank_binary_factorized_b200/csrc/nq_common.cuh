@@ -44,6 +44,14 @@ __device__ __forceinline__ uint16_t float_to_bf16_bits(float f) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
+// Two fp32 -> two bf16 in one register (lo in the low half), each rounded to nearest even: one
+// conversion instruction for the pair.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Programmatic dependent launch: wait for the grid queued before this one to finish and
 // publish its memory, and let the next grid start its prologue.  Both are no-ops when the
 // kernel was launched without the programmatic-serialisation attribute.
