@@ -73,24 +73,25 @@ __device__ __forceinline__ void adapter_bounds(const int32_t* offsets, int n, in
 }
 
 // Tile number `tile` when every adapter's rows are cut into tiles of rows_per_tile and those
-// without one into tiles of none_per_tile, groups in order.  A whole warp calls it; 128 groups are
-// scanned at a time, four neighbours a lane.
-__device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, int64_t M, int rows_per_tile,
-                                                 int none_per_tile, int tile, unsigned int* err) {
+// without one into tiles of none_per_tile, groups in order.  A whole warp calls it; 32 L groups are
+// scanned at a time, L neighbours a lane.
+template <int L>
+__device__ __forceinline__ AdapterTile find_tile_by(const int32_t* offsets, int n, int64_t M, int rows_per_tile,
+                                                    int none_per_tile, int tile, unsigned int* err) {
     const int lane = threadIdx.x & 31;
     int before = 0;  // tiles of the groups before this batch
     int padded = 0;  // and their rows in multiples of 16
-    for (int a0 = 0; a0 <= n; a0 += 128) {
-        int first[4], last[4], tiles[4], mine = 0, rows16 = 0;
+    for (int a0 = 0; a0 <= n; a0 += 32 * L) {
+        int first[L], last[L], tiles[L], mine = 0, rows16 = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int a = a0 + 4 * lane + i;
+        for (int i = 0; i < L; ++i) {
+            const int a = a0 + L * lane + i;
             first[i] = last[i] = 0;
             if (a <= n) adapter_bounds(offsets, n, M, a, first[i], last[i], err);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int per = a0 + 4 * lane + i < n ? rows_per_tile : none_per_tile;
+        for (int i = 0; i < L; ++i) {
+            const int per = a0 + L * lane + i < n ? rows_per_tile : none_per_tile;
             tiles[i] = (last[i] - first[i] + per - 1) / per;
             mine += tiles[i];
             rows16 += (last[i] - first[i] + 15) & ~15;
@@ -107,16 +108,16 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
             const int src = __ffs(hit) - 1;
             AdapterTile t;
             t.padded = padded + static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < src ? rows16 : 0));
-            // the lane that has it looks through its four groups
+            // the lane that has it looks through its groups
             int rest = local - (upto - mine);
             t.adapter = -1;
             t.first = t.count = 0;
             int in_lane = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < L; ++i) {
                 if (t.adapter < 0 && rest < tiles[i]) {
-                    const int per = a0 + 4 * lane + i < n ? rows_per_tile : none_per_tile;
-                    t.adapter = a0 + 4 * lane + i;
+                    const int per = a0 + L * lane + i < n ? rows_per_tile : none_per_tile;
+                    t.adapter = a0 + L * lane + i;
                     t.first = first[i] + rest * per;
                     t.count = min(per, last[i] - t.first);
                     in_lane += rest * per;
@@ -135,6 +136,13 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
         padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rows16));
     }
     return {-1, 0, 0, 0};
+}
+
+// One group a lane where that is all of them (the common case, with the least latency).
+__device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, int64_t M, int rows_per_tile,
+                                                 int none_per_tile, int tile, unsigned int* err) {
+    return n < 32 ? find_tile_by<1>(offsets, n, M, rows_per_tile, none_per_tile, tile, err)
+                  : find_tile_by<4>(offsets, n, M, rows_per_tile, none_per_tile, tile, err);
 }
 
 // Adapter a's bounds in `rows` and its first padded row.  A whole warp calls it.
