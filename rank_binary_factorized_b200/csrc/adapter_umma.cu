@@ -8,8 +8,8 @@
 // arranged so that the loads never pause.  One launch does both products:
 //
 // - A tile is up to 128 rows that share an adapter; the rows may lie anywhere (TMA row gathers).  A
-//   cluster of CS blocks takes a tile; block q multiplies K-blocks [KB q / CS, KB (q + 1) / CS) of 64
-//   in the first product and column blocks of 64 in the second, so a few tiles still use most SMs.
+//   cluster of CS blocks takes a tile; a block multiplies every CS-th K-block of 64 in the first
+//   product and column block of 64 in the second, so a few tiles still use most SMs.
 // - Warp 0 loads, warp 1 issues the MMAs, warps 2..5 are the epilogue.  One ring of slots serves both
 //   products (a 128 x 64 tile of z, or of base, and the matching tile of P or Q), so the loads of
 //   the second product, and of the cluster's next tile, are in flight while t is put together.
@@ -135,9 +135,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
 
     const int kb_all = static_cast<int>((a.K + kStep - 1) / kStep), nb_all = static_cast<int>((a.N + kStep - 1) / kStep);
-    const int kb0 = kb_all * static_cast<int>(q) / static_cast<int>(cs), kb1 = kb_all * (static_cast<int>(q) + 1) / static_cast<int>(cs);
-    const int nb0 = a.out ? nb_all * static_cast<int>(q) / static_cast<int>(cs) : 0;
-    const int nb1 = a.out ? nb_all * (static_cast<int>(q) + 1) / static_cast<int>(cs) : 0;
+    // Block q takes every cs-th block of 64 from q on: the cluster reads and writes neighbouring pieces of
+    // a row at about the same time (1% faster than a range for each block, at 8192 rows of a 70B gate).
+    const int kb_n = (kb_all - static_cast<int>(q) + static_cast<int>(cs) - 1) / static_cast<int>(cs);
+    const int nb_n = a.out ? (nb_all - static_cast<int>(q) + static_cast<int>(cs) - 1) / static_cast<int>(cs) : 0;
+    auto col_at = [&](int i) { return (i * static_cast<int>(cs) + static_cast<int>(q)) * kStep; };
     const uint32_t w1_bytes = BWD ? panels * 8192u : r16 * 128u;
     const uint32_t w2_bytes = BWD ? r16 * 128u : panels * 8192u;
     pdl_wait();
@@ -195,15 +197,15 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) row0[g] = __shfl_sync(0xFFFFFFFFu, row[0], 8 * g);
             // the tile of P or Q that goes with column block b, by one thread
-            auto load_w = [&](auto second, int b, uint32_t w, uint32_t bar) {
+            auto load_w = [&](auto second, int col, uint32_t w, uint32_t bar) {
                 if constexpr (second.value == BWD) {  // A: [rank][64 of d_in]
-                    tc::tma_load_3d(w, &map_a, b * kStep, 0, t.adapter, bar);
+                    tc::tma_load_3d(w, &map_a, col, 0, t.adapter, bar);
                 } else {  // B: [64 of d_out][rank], in panels of 64 ranks
-                    tc::tma_load_3d(w, &map_b, 0, b * kStep, t.adapter, bar);
-                    if (panels > 1) tc::tma_load_3d(w + 8192u, &map_b, 64, b * kStep, t.adapter, bar);
+                    tc::tma_load_3d(w, &map_b, 0, col, t.adapter, bar);
+                    if (panels > 1) tc::tma_load_3d(w + 8192u, &map_b, 64, col, t.adapter, bar);
                 }
             };
-            auto load_all = [&](auto second, int b0, int b1) {
+            auto load_all = [&](auto second, int blocks) {
                 constexpr bool kSecond = second.value;
                 const CUtensorMap* box_map = kSecond ? &map_base : &map_z;
                 const CUtensorMap* box32_map = kSecond ? &map_base32 : &map_z32;
@@ -212,20 +214,21 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 if (boxes) {
                     const bool me = tc::elect_one();
                     if (me) {
-                        for (int b = b0; b < b1; ++b) {
+                        for (int b = 0; b < blocks; ++b) {
                             next(kSecond);
                             if (!ok) break;
+                            const int col = col_at(b);
                             const uint32_t tok = slot_at(s), bar = full(s);
                             tc::mbar_arrive_expect_tx(bar, bytes);
                             if (whole) {
-                                tc::tma_load_2d(tok, box_map, b * kStep, tile_row0, bar);
+                                tc::tma_load_2d(tok, box_map, col, tile_row0, bar);
                             } else {
 #pragma unroll
                                 for (int g = 0; g < 4; ++g)
                                     if (32 * g < t.count)
-                                        tc::tma_load_2d(tok + g * 4096u, box32_map, b * kStep, row0[g], bar);
+                                        tc::tma_load_2d(tok + g * 4096u, box32_map, col, row0[g], bar);
                             }
-                            load_w(second, b, tok + kTokBytes, bar);
+                            load_w(second, col, tok + kTokBytes, bar);
                             advance();
                         }
                     }
@@ -237,29 +240,30 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     ph2 = __shfl_sync(0xFFFFFFFFu, ph2, src);
                     ok = __shfl_sync(0xFFFFFFFFu, ok, src);
                 } else {
-                    for (int b = b0; b < b1; ++b) {
+                    for (int b = 0; b < blocks; ++b) {
                         next(kSecond);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
+                        const int col = col_at(b);
                         const uint32_t tok = slot_at(s), bar = full(s);
                         if (tc::elect_one()) {
                             tc::mbar_arrive_expect_tx(bar, bytes);
-                            load_w(second, b, tok + kTokBytes, bar);
+                            load_w(second, col, tok + kTokBytes, bar);
                         }
                         __syncwarp();
                         if (loads) {
                             if (box)
-                                tc::tma_load_2d(tok + lane * 512u, box32_map, b * kStep, row[0], bar);
+                                tc::tma_load_2d(tok + lane * 512u, box32_map, col, row[0], bar);
                             else
-                                tc::tma_gather4(tok + lane * 512u, row_map, b * kStep, row, bar);
+                                tc::tma_gather4(tok + lane * 512u, row_map, col, row, bar);
                         }
                         __syncwarp();
                         advance();
                     }
                 }
             };
-            load_all(std::false_type{}, kb0, kb1);
-            if (ok) load_all(std::true_type{}, nb0, nb1);
+            load_all(std::false_type{}, kb_n);
+            if (ok) load_all(std::true_type{}, nb_n);
         }
         // every load issued has landed before the block may end
         if (lane == 0) {
@@ -290,25 +294,25 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (me) {
                 uint32_t jt = it, jacc = acc2;
                 int js = s;
-                if (kb1 > kb0) {
+                if (kb_n > 0) {
                     ok = tc::mbar_wait(acc1_empty, (tiles & 1u) ^ 1u, err);
-                    for (int b = kb0; b < kb1 && ok; ++b, ++jt) {
+                    for (int b = 0; b < kb_n && ok; ++b, ++jt) {
                         if (!(ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err))) break;
                         tc::tc_fence_after();
                         const uint32_t off = js * (ua.slot_bytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kStep / 16; ++kk)
                             tc::mma_f16_ss(tmem, tok_desc + off + kk * 2u, w1_desc + off + kk * (BWD ? 128u : 2u), idesc1,
-                                           (b > kb0 || kk > 0) ? 1u : 0u);
+                                           (b > 0 || kk > 0) ? 1u : 0u);
                         tc::mma_commit(free1(js));
                         if (++js == slots) js = 0;
                     }
                     if (ok) tc::mma_commit(acc1_full);
                 }
-                if (ok && nb1 > nb0) {
+                if (ok && nb_n > 0) {
                     ok = tc::mbar_wait(t_full, tiles & 1u, err);
                     tc::fence_proxy_async_smem();  // t was written by threads
-                    for (int b = nb0; b < nb1 && ok; ++b, ++jt, ++jacc) {
+                    for (int b = 0; b < nb_n && ok; ++b, ++jt, ++jacc) {
                         const uint32_t i = jacc & 1;
                         ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err) &&
                              tc::mbar_wait(acc2_empty(i), ((jacc >> 1) & 1u) ^ 1u, err);
@@ -330,8 +334,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 }
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1);
-            it += (kb1 - kb0) + (nb1 - nb0);
-            acc2 += nb1 - nb0;
+            it += kb_n + nb_n;
+            acc2 += nb_n;
             s = it % slots;
             ++tiles;
         }
@@ -366,8 +370,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     for (int r = 0; r < a.rank; ++r) a.t[static_cast<int64_t>(my_row) * a.rank + r] = 0.f;
                 if (a.out && a.out != a.base) {
                     // 16 rows, pieces of 16 bytes side by side over the epilogue's threads
-                    const int64_t c0 = static_cast<int64_t>(nb0) * kStep;
-                    const int pieces = static_cast<int>((min(a.N, static_cast<int64_t>(nb1) * kStep) - c0) / 8);
+                    const int64_t c0 = static_cast<int64_t>(nb_all) * q / cs * kStep;
+                    const int pieces = static_cast<int>((min(a.N, static_cast<int64_t>(nb_all) * (q + 1) / cs * kStep) - c0) / 8);
                     for (int m0 = 0; m0 < t.count; m0 += 4) {
                         int row[4];
 #pragma unroll
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 __syncwarp();
                 ok = ok && tc::mbar_wait(peers_ready, (tiles & 1u) ^ 1u, err);
             }
-            if (ok && kb1 > kb0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
+            if (ok && kb_n > 0) ok = tc::mbar_wait(acc1_full, tiles & 1u, err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc::tc_fence_after();
             // this lane's group of 8 rows, the block that owns it and its place there
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const uint32_t at = (my_group - owner_first) * 1024u;
             for (int g = set; g < segs && ok; g += 2) {
                 uint32_t v[32];
-                if (kb1 > kb0) {
+                if (kb_n > 0) {
                     tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + g * 32, v);
                     tc::tmem_wait_ld();
                 } else {
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (kb1 > kb0) tc::mbar_arrive(acc1_empty);
+                if (kb_n > 0) tc::mbar_arrive(acc1_empty);
                 if (eid == 0)
                     tc::mbar_arrive_expect_tx(inbox_full, (cs - 1) * own_rows * r16 * 4u);
                 else
@@ -531,10 +535,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             __syncwarp();
             if (eid == 0) tc::mbar_arrive_expect_tx(t_full, (16 - own_groups) * 2 * panels * 1024u);
             // ---- out = base + the second product
-            it += kb1 - kb0;
+            it += kb_n;
             s = it % slots;
             uint8_t* mine = smem_raw + (staging - tc::smem_u32(smem_raw)) + (warp - 2) * 4096;
-            for (int b = nb0; b < nb1 && ok; ++b, ++acc2) {
+            for (int b = 0; b < nb_n && ok; ++b, ++acc2) {
                 const int i = acc2 & 1;
                 if (i != set) {
                     ++it;
@@ -574,13 +578,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tc::tma_store_2d(&map_out, staging + (warp - 2) * 4096u, b * kStep, row0);
+                        tc::tma_store_2d(&map_out, staging + (warp - 2) * 4096u, col_at(b), row0);
                         tc::bulk_commit_group();
                     }
                 } else {
                     __syncwarp();
                     // eight lanes store the 128 bytes of a row
-                    const int64_t col = static_cast<int64_t>(b) * kStep + (lane & 7) * 8;
+                    const int64_t col = col_at(b) + (lane & 7) * 8;
 #pragma unroll
                     for (int g = 0; g < 8; ++g)
                         y[g] = *reinterpret_cast<const uint4*>(mine + (g * 4 + (lane >> 3)) * 128 +

@@ -532,8 +532,9 @@ def adapter_rows(ids: torch.Tensor, n: int, stream=None) -> AdapterRows:
 
 def _call(name: str, fn, device, stream, *args) -> None:
     """Calls the library with the tensors' device current, on `stream` or that device's current one."""
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
             status = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
@@ -544,7 +545,7 @@ def _call(name: str, fn, device, stream, *args) -> None:
 def _rows_ptr(t, name: str, dtype, M: int, cols: int, device) -> int:
     """The address of a contiguous [M][cols] tensor on `device`; _need says what is wrong with another."""
     try:
-        if t.dtype is dtype and t.device == device and t.shape == (M, cols) and t.is_contiguous():
+        if t.dtype is dtype and t.get_device() == device.index and t.shape == (M, cols) and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -555,7 +556,7 @@ def _rows_ptr(t, name: str, dtype, M: int, cols: int, device) -> int:
 def _array_ptr(t, name: str, dtype, shape, device) -> int:
     """The same for any shape."""
     try:
-        if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        if t.dtype is dtype and t.get_device() == device.index and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -565,7 +566,7 @@ def _array_ptr(t, name: str, dtype, shape, device) -> int:
 
 def _ws_ptr(ws, device) -> int:
     try:
-        if ws.dtype is torch.uint8 and ws.device == device and ws.is_contiguous():
+        if ws.dtype is torch.uint8 and ws.get_device() == device.index and ws.is_contiguous():
             return ws.data_ptr()
     except AttributeError:
         pass
