@@ -274,7 +274,8 @@ NQ_API nq_status nq_silu_mul(const uint16_t* g, const uint16_t* u, uint16_t* h, 
  *
  * n adapters of one projection, all of one rank (lower ranks are padded with zero rows of A or
  * zero columns of B).  1 <= n <= NQ_ADAPTER_MAX_N, 1 <= rank <= NQ_ADAPTER_MAX_RANK.
- * Fastest where d_in, d_out, rank, lda and ldb are multiples of 8; any value works.
+ * Any value works; d_in, d_out, lda and ldb in multiples of 8 let batches run on the tensor cores
+ * (others, and small groups of rows, run on the CUDA cores).
  */
 #define NQ_ADAPTER_MAX_RANK 128
 #define NQ_ADAPTER_MAX_N 16384
@@ -304,13 +305,15 @@ NQ_API nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32
 /*
  * nq_adapter_forward -- for every row m with adapter a:
  *     t[m] = scale_a A_a x[m],   out[m] = bf16( y[m] + B_a t[m] );
- * a row without an adapter gets out[m] = y[m] and t[m] = 0, and its x[m] is not read.
+ * a row without an adapter gets out[m] = y[m] and t[m] = 0, whatever its x[m] holds.
  *   x [M][d_in], y and out [M][d_out] bf16; out may be y.  t [M][rank] fp32, or NULL: what
  *   nq_adapter_backward takes.  rows, offsets: as nq_adapter_rows writes them.  Each row must be
  *   listed once: a row that is not listed is left as it was, and a row listed more than once is
  *   left undefined.  A list entry outside 0..M-1 or offsets out of order are skipped and make the
  *   next nq_sync_status return NQ_ERR_INDEX; no memory outside the arguments is touched.
- * Sums are fp32 in a fixed order (run-to-run identical); out is rounded once.  Needs no workspace.
+ * Sums are fp32 in a fixed order (run-to-run identical); out is rounded once.  On the tensor cores t
+ * enters the second product as the sum of two bf16 values, which keeps 16 of its bits.  Needs no
+ * workspace.
  */
 NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets,
                                     const uint16_t* x, const uint16_t* y, uint16_t* out, float* t, int64_t M,
@@ -325,9 +328,8 @@ NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, c
  *   xbar_out may be xbar.  t: as nq_adapter_forward wrote it (it includes the scale).  gA and gB
  *   are written whole, zeros for an adapter without rows.  xbar_out (then xbar too), gA and gB
  *   may each be NULL; t is needed for gB, x for gA.
- * Sums are fp32 in a fixed order; every output is rounded once to bf16.  Where tensor cores are
- * used (widths in multiples of 8), t and u enter the second products as the sum of two bf16
- * values, which keeps 16 of their bits.  ws: nq_adapter_workspace_bytes(S, M) bytes (0 for invalid
+ * Sums are fp32 in a fixed order; every output is rounded once to bf16.  On the tensor cores t and u
+ * enter the second products as the sum of two bf16 values, which keeps 16 of their bits.  ws: nq_adapter_workspace_bytes(S, M) bytes (0 for invalid
  * adapters or M).
  */
 NQ_API size_t nq_adapter_workspace_bytes(const nq_adapters* S, int64_t M);

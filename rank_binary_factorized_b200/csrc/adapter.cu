@@ -5,11 +5,14 @@
 //   u[m] = scale_a B_a^T ybar[m],   xbar'[m] = xbar[m] + A_a^T u[m]
 //   gA_a = sum_m u[m] x[m]^T,   gB_a = sum_m ybar[m] t[m]^T
 //
-// A decode step is bound by reading A_a and B_a once, and at its smallest by the launch, so one
-// launch does both products: a cluster of blocks takes a tile of up to 8 rows that share an
-// adapter, each block a slice of the first product's length K and of the second's outputs N.  The
-// blocks' partial t meet in distributed shared memory between the two.  Sums are fp32 in a fixed
-// order; out is rounded once.
+// A decode step is bound by reading A_a and B_a once, and at its smallest by the latency of a launch and
+// two dependent reads, so one launch does both products: a cluster of up to 16 blocks takes a tile
+// of up to 8 rows that share an adapter, each block a slice of the first product's length K and of
+// the second's outputs N, and the blocks' partial t meet in distributed shared memory between the
+// two.  Tiles of 8: a decode batch has few rows an adapter, and 8 rows' sums fit the registers.
+// Sums are fp32 in a fixed order; out is rounded once.
+// Measured (B200, in a CUDA graph): one row of 4096 x 4096 at rank 16 5.7 us, of a 70B gate at rank 64
+// 11 us (4.7 MB); 64 rows of 64 adapters at 8192 x 8192, rank 16, 11 us (36.7 MB, 3.3 TB/s).
 #include "adapter.cuh"
 #include "tc_common.cuh"
 
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(256) adapter_grad_any_kernel(const AdapterGrad
 // Few rows an adapter: bound by writing gA and gB, 16 bytes a thread at a time, neighbouring threads side
 // by side.  A block has one adapter and either 8 ranks of 2048 columns of gA or a run of gB, and takes the tokens
 // 8 at a time.  Widths and rank in multiples of 8.
+// Measured: 64 adapters of 8192 x 8192 at rank 16 (33.5 MB of gradients) 18 us after u is there.
 constexpr int kSmallTokens = 8;
 constexpr int kSmallRanks = 8;    // ranks of gA of a block
 constexpr int kSmallPieces = 4;   // 16-byte pieces of gB of a thread

@@ -10,14 +10,19 @@
 // - A tile is up to 128 rows that share an adapter; the rows may lie anywhere (TMA row gathers).  A
 //   cluster of CS blocks takes a tile; a block multiplies every CS-th K-block of 64 in the first
 //   product and column block of 64 in the second, so a few tiles still use most SMs.
-// - Warp 0 loads, warp 1 issues the MMAs, warps 2..5 are the epilogue.  One ring of slots serves both
+// - Warp 0 loads, warp 1 issues the MMAs, warps 2..9 are the epilogue.  One ring of slots serves both
 //   products (a 128 x 64 tile of z, or of base, and the matching tile of P or Q), so the loads of
 //   the second product, and of the cluster's next tile, are in flight while t is put together.
-// - The blocks' partial t go to the block that owns the row (128 / CS rows each) through distributed
-//   shared memory; it adds them in rank order, scales, writes t and sends the row to every block as
-//   the sum of two bf16 values (16 bits of t: rounding t itself to bf16 would add half a unit of its
-//   own to the result), in the layout that the second product's A operand has.
-// - The epilogue adds the accumulator to the tile of base in shared memory and stores whole row pieces.
+// - The blocks' partial t go to the block that owns the row by bulk copies between their shared memories
+//   (plain remote stores of the same took three times as long); it adds them in rank order, scales,
+//   writes t and sends its rows to every block as the sum of two bf16 values (16 bits of t: rounding
+//   t itself to bf16 would add half a unit of its own to the result), in the layout that the second
+//   product's A operand has.
+// - The epilogue adds the accumulator to the tile of base in registers and stores it from a staging tile
+//   of its own, so that a slot is free as soon as it is read.
+// Measured (B200): 8192 rows of a 70B gate (8192 -> 28672) at rank 64 193 us, 1.09 GB at 5.6 TB/s, 0.85 of the
+// measured copy rate; 5000 rows of 8192 x 8192 at rank 16 50 us (4.9 TB/s); one tile alone 15 to 20 us
+// (some 4 us to the first tile's data, 3 us between the products).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

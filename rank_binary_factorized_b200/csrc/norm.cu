@@ -13,6 +13,12 @@
 //   gy  = (w_post dz - y^ c(w_post dz, y^)) / q(y)  (post_norm; else dz),  g_w_post = sum_m dz y^
 //
 // Everything between the loads and the stores is fp32; each output is rounded once.
+//
+// Bound: HBM, 6 to 14 bytes an element forward and 12 to 20 backward.  Measured (B200): 16384 rows of 8192
+// with an fp32 residual and a gate per row 286 us, 1.88 GB at 6.57 TB/s, the measured copy rate;
+// gradients of 8192 x 8192 bf16 135 us and 9 us for the vectors' sums, 0.81 GB at 5.6 TB/s; one row of
+// 8192 3.7 us forward, 8.8 us backward.  Rows that do not start on 16 bytes (an odd d) cost the
+// arithmetic of the shifts: 16384 x 8191 356 us forward (3.0 TB/s), 616 us backward (2.6 TB/s).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -955,7 +961,10 @@ nq_status nq_launch_block_norm(const nq::NormFwdArgs& a, int64_t M, cudaStream_t
     void* kargs[] = {&args, nullptr, nullptr};
     const bool row_gate = a.gate && a.ld_gate > 0;
     const bool shift = a.d % 8 != 0 || a.ld_gate % 8 != 0;
-    if (a.d <= kRingMaxD && M > 2 * static_cast<int64_t>(nq_host::sm_count()) && !(row_gate && a.ld_gate != a.d)) {
+    // One block per row while about 1000 threads a multiprocessor hold them all at once (3.6 us at 296 rows
+    // of 4096 and at 1100 of 1024), the ring above that (5.3 us at 300 and at 1190 rows).
+    const bool one_wave = M * row_threads(a.d, 8) <= 1024 * static_cast<int64_t>(nq_host::sm_count());
+    if (a.d <= kRingMaxD && !one_wave && !(row_gate && a.ld_gate != a.d)) {
         nq::NormRing ring{};
         ring.s16[0] = a.y;
         ring.s16[1] = row_gate ? a.gate : nullptr;
