@@ -49,7 +49,7 @@ SHAPES = [(1, 64, 96, 8, 1), (1, 5, 3, 1, 1), (7, 17, 33, 3, 4), (9, 256, 264, 1
           (129, 8, 8, 8, 1),
           # 17 to 150 tiles: every number of blocks that share one
           (2100, 640, 712, 16, 1), (3000, 576, 136, 24, 2), (4100, 136, 520, 64, 2), (5000, 584, 600, 8, 1),
-          (9000, 72, 136, 40, 3), (19000, 136, 72, 16, 2), (2100, 640, 520, 128, 1)]
+          (9000, 72, 136, 40, 3), (700, 64, 72, 8, 1200), (700, 136, 72, 16, 100), (19000, 136, 72, 16, 2), (2100, 640, 520, 128, 1)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
