@@ -209,13 +209,34 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
                             }
                         }
                     }
+                    // over the lanes along K; while a lane has several sums, the two of a pair keep half each
+                    constexpr int kSums = NT * V;
+                    float(&sum)[kSums] = reinterpret_cast<float(&)[kSums]>(acc);
+                    int kept = 0;         // index of sum[0]
+                    bool writes = true;   // of the lanes that end with the same sum, the lowest
 #pragma unroll
-                    for (int m = 0; m < NT; ++m)
+                    for (int st = 0; st < 5; ++st) {
+                        const int o = 16 >> st, w = kSums >> (st + 1);
+                        if (o < side) break;  // the same for every lane
+                        const bool upper = lane & o;
+                        if (w >= 1) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            for (int o = 16; o >= side; o /= 2) acc[m][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[m][i], o);
-                            if (lane < side && r0 + i < R) s.warp_part[warp][m][r0 + i] = acc[m][i];
+                            for (int j = 0; j < w; ++j) {
+                                const float keep = upper ? sum[j + w] : sum[j], give = upper ? sum[j] : sum[j + w];
+                                sum[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                            }
+                            kept += upper ? w : 0;
+                        } else {
+                            sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], o);
+                            writes = writes && !upper;
                         }
+                    }
+                    const int left = max(1, kSums / along);
+#pragma unroll
+                    for (int j = 0; j < kSums; ++j) {
+                        const int m = (kept + j) / V, i = (kept + j) % V;
+                        if (j < left && writes && r0 + i < R) s.warp_part[warp][m][r0 + i] = sum[j];
+                    }
                 }
                 __syncthreads();
                 for (int e = threadIdx.x; e < NT * R; e += kRowsThreads) {
@@ -355,7 +376,7 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
             int share = 1;
             while (V == 8 && share < 8 && 2 * share * vecs <= kRowsThreads) share *= 2;
             const int per = kRowsThreads / share, g = threadIdx.x / per;
-            float* sums = &s.warp_part[0][0][0];  // [share][per][V]
+            float* sums = &s.warp_part[0][0][0];  // [V][threads]
             for (int v0 = 0; v0 < vecs; v0 += per) {
                 const int64_t j = n_begin + static_cast<int64_t>(v0 + threadIdx.x % per) * V;
                 const bool in = j < n_end;
@@ -394,12 +415,12 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
                     for (int m = 0; m < NT; ++m) {
                         __syncthreads();
 #pragma unroll
-                        for (int i = 0; i < V; ++i) sums[threadIdx.x * V + i] = acc[m][i];
+                        for (int i = 0; i < V; ++i) sums[i * kRowsThreads + threadIdx.x] = acc[m][i];
                         __syncthreads();
                         if (g == 0)
                             for (int h = 1; h < share; ++h)
 #pragma unroll
-                                for (int i = 0; i < V; ++i) acc[m][i] += sums[(h * per + threadIdx.x) * V + i];
+                                for (int i = 0; i < V; ++i) acc[m][i] += sums[i * kRowsThreads + h * per + threadIdx.x];
                     }
                 }
                 if (in && g == 0) {

@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         b0 = static_cast<int>(all * sp / wa.splits);
         b1 = static_cast<int>(all * (sp + 1) / wa.splits);
     };
-    pdl_wait();
-    pdl_launch_dependents();
+    // The lists were written before the launch ahead of this one, which waited for its own predecessors
+    // before it let this one start: they may be read before that launch is over.
     if (kept) {
         if (warp == 0) {
             int padded = 0;
@@ -129,6 +129,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         }
         __syncthreads();
     }
+    pdl_wait();
+    pdl_launch_dependents();
     // The blocks take units in turn, there and back, from the longest adapter's on: a block's last unit is
     // short where its others were long.
     auto unit_of = [&](int64_t round) {

@@ -485,14 +485,15 @@ nq::AdapterArgs adapter_args(const nq_adapters* S, const int32_t* rows, const in
 }
 
 // The two products run on the tensor cores (tiles of 128 rows of an adapter) or on the CUDA cores (tiles
-// of 8).  Few rows for each loaded adapter, or (forward) few rows times rank at all, are for the
-// latter: there a tile costs little beyond reading its adapter, while the tensor cores' tile takes
-// some 20 us from start to end.  Measured at 8192 x 8192, CUDA cores and tensor cores: forward, rank
-// 16: 64 rows of 64 adapters 11 and 70 us, 64 rows of one 12 and 19, 256 of 64 24 and 69; rank 64: 4
-// rows of one 13 and 22, 64 of one 26 and 21; backward, rank 16: 64 rows of 64 10 and 71, of one 21
-// and 20; at 4096 x 4096, rank 128, 8 rows of one 20 and 17.
+// of 8).  Few rows for each loaded adapter, or few rows times rank at all, are for the latter: there a
+// tile costs little beyond reading its adapter, while the tensor cores' tile takes some 20 us from
+// start to end.  Measured at 8192 x 8192, CUDA cores and tensor cores: forward, rank 16: 64 rows of 64
+// adapters 11 and 70 us, 64 rows of one 12 and 19, 256 of 64 24 and 69; rank 64: 4 rows of one 13 and
+// 22, 64 of one 26 and 21; backward, rank 16: 64 rows of 64 9 and 71, of 8 16 and 23, 128 of one 22
+// and 19; at 4096 x 4096, rank 128, 8 rows of one 20 and 17.
 bool products_on_tensor_cores(const nq::AdapterArgs& a, bool backward) {
-    const bool few = a.M <= 512 && (a.M <= 8 * static_cast<int64_t>(a.n) || (!backward && a.M * a.rank <= 1024));
+    const bool few = a.M <= 512 && (a.M <= 8 * static_cast<int64_t>(a.n) ||
+                                    (a.M * a.rank <= 1024 && (a.M <= 64 || !backward)));
     return !(few && (a.rank <= 64 || a.M <= 4)) && nq_adapter_umma_fits(a);
 }
 

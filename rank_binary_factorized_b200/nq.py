@@ -11,6 +11,9 @@ Tensor conventions (device tensors, contiguous):
   s1, s2        float16 [d_out], [d_in]
   x, y          bfloat16 [M][d_in], [M][d_out]
   latent        float32 [rows][ld_latent]
+  adapters      A bfloat16 [n][rank][d_in], B bfloat16 [n][d_out][rank], scale float32 [n]
+  row lists     int32 (ids [M], rows [M], offsets [n + 1])
+  block norms   y, x, gate bfloat16, the residual stream bfloat16 or float32
 """
 from __future__ import annotations
 
