@@ -424,7 +424,8 @@ nq_status nq_launch_adapter_wgrad_umma(const nq::AdapterGradArgs& g, const uint1
     const uint16_t* x = g.gA ? g.x : g.ybar;
     const uint16_t* y = g.gB ? g.ybar : g.x;
     const int64_t xd[2] = {g.gA ? g.d_in : g.d_out, g.M}, yd[2] = {g.gB ? g.d_out : g.d_in, g.M};
-    const int64_t ld = part_ld, pd[2] = {part_ld, 2 * part_rows};
+    // columns past the rank (in 16s) are not read: the boxes get zeros there
+    const int64_t ld = part_ld, pd[2] = {wa.r16, 2 * part_rows};
     if (!nq_host::tmap_bf16(&x64, x, 2, xd, xd, b64) || !nq_host::tmap_bf16(&x32, x, 2, xd, xd, b32) ||
         !nq_host::tmap_bf16(&x1, x, 2, xd, xd, b1) || !nq_host::tmap_bf16(&y64, y, 2, yd, yd, b64) ||
         !nq_host::tmap_bf16(&y32, y, 2, yd, yd, b32) || !nq_host::tmap_bf16(&y1, y, 2, yd, yd, b1) ||
