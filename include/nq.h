@@ -309,8 +309,9 @@ NQ_API nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32
  *   x [M][d_in], y and out [M][d_out] bf16; out may be y.  t [M][rank] fp32, or NULL: what
  *   nq_adapter_backward takes.  rows, offsets: as nq_adapter_rows writes them.  Each row must be
  *   listed once: a row that is not listed is left as it was, and a row listed more than once is
- *   left undefined.  A list entry outside 0..M-1 or offsets out of order are skipped and make the
- *   next nq_sync_status return NQ_ERR_INDEX; no memory outside the arguments is touched.
+ *   left undefined.  A list entry outside 0..M-1 is skipped; from the first two offsets out of order
+ *   on, the groups count as empty (their adapters' gradients are undefined).  Both make the next
+ *   nq_sync_status return NQ_ERR_INDEX; no memory outside the arguments is touched.
  * Sums are fp32 in a fixed order (run-to-run identical); out is rounded once.  On the tensor cores t
  * enters the second product as the sum of two bf16 values, which keeps 16 of its bits.  Needs no
  * workspace.
@@ -329,8 +330,8 @@ NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, c
  *   are written whole, zeros for an adapter without rows.  xbar_out (then xbar too), gA and gB
  *   may each be NULL; t is needed for gB, x for gA.
  * Sums are fp32 in a fixed order; every output is rounded once to bf16.  On the tensor cores t and u
- * enter the second products as the sum of two bf16 values, which keeps 16 of their bits.  ws: nq_adapter_workspace_bytes(S, M) bytes (0 for invalid
- * adapters or M).
+ * enter the second products as the sum of two bf16 values, which keeps 16 of their bits.
+ * ws: nq_adapter_workspace_bytes(S, M) bytes (0 for invalid adapters or M).
  */
 NQ_API size_t nq_adapter_workspace_bytes(const nq_adapters* S, int64_t M);
 NQ_API nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets,

@@ -62,14 +62,17 @@ struct AdapterTile {
 
 // Bounds of adapter a's entries in `rows`, forced into 0 <= first <= last <= M whatever the
 // offsets say; a == n: the rows after the last adapter's.  Offsets outside that order are
-// reported.
-__device__ __forceinline__ void adapter_bounds(const int32_t* offsets, int n, int64_t M, int a, int& first, int& last,
+// reported, and false is returned.  Groups whose predecessors are all in order hold M rows at most between
+// them; one pair alone says nothing about that (0, M, 0, M), so the scans below count every
+// group from the first bad pair on as empty.
+__device__ __forceinline__ bool adapter_bounds(const int32_t* offsets, int n, int64_t M, int a, int& first, int& last,
                                                unsigned int* err) {
     const int64_t lo = offsets[a], hi = a < n ? static_cast<int64_t>(offsets[a + 1]) : M;
     const bool ok = lo >= 0 && lo <= hi && hi <= M && (a > 0 || lo == 0);
     if (!ok) flag_error(err, kErrIndex);
     first = static_cast<int>(ok ? lo : 0);
     last = static_cast<int>(ok ? hi : 0);
+    return ok;
 }
 
 // Tile number `tile` when every adapter's rows are cut into tiles of rows_per_tile and those
@@ -83,11 +86,18 @@ __device__ __forceinline__ AdapterTile find_tile_by(const int32_t* offsets, int 
     int padded = 0;  // and their rows in multiples of 16
     for (int a0 = 0; a0 <= n; a0 += 32 * L) {
         int first[L], last[L], tiles[L], mine = 0, rows16 = 0;
+        bool ok = true;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const int a = a0 + L * lane + i;
             first[i] = last[i] = 0;
-            if (a <= n) adapter_bounds(offsets, n, M, a, first[i], last[i], err);
+            if (a <= n) ok = adapter_bounds(offsets, n, M, a, first[i], last[i], err) && ok;
+            if (!ok) first[i] = last[i] = 0;
+        }
+        const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok);
+        if (bad != 0u && lane >= __ffs(bad)) {  // lanes after the first with a bad pair
+#pragma unroll
+            for (int i = 0; i < L; ++i) first[i] = last[i] = 0;
         }
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -132,6 +142,7 @@ __device__ __forceinline__ AdapterTile find_tile_by(const int32_t* offsets, int 
             t.padded += __shfl_sync(0xFFFFFFFFu, in_lane, src);
             return t;
         }
+        if (bad != 0u) break;
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
         padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rows16));
     }
@@ -145,14 +156,18 @@ __device__ __forceinline__ AdapterTile find_tile(const int32_t* offsets, int n, 
                   : find_tile_by<4>(offsets, n, M, rows_per_tile, none_per_tile, tile, err);
 }
 
-// Adapter a's bounds in `rows` and its first padded row.  A whole warp calls it.
+// Adapter a's bounds in `rows` and its first padded row; no rows after a bad pair.  A whole warp calls it.
 __device__ __forceinline__ int find_group(const int32_t* offsets, int n, int64_t M, int adapter, int& first, int& last,
                                           unsigned int* err) {
     const int lane = threadIdx.x & 31;
     int padded = 0;
     for (int a0 = 0; a0 < adapter; a0 += 32) {
         int f = 0, l = 0;
-        if (a0 + lane < adapter) adapter_bounds(offsets, n, M, a0 + lane, f, l, err);
+        const bool ok = a0 + lane >= adapter || adapter_bounds(offsets, n, M, a0 + lane, f, l, err);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+            first = last = 0;
+            return 0;
+        }
         padded += static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, (l - f + 15) & ~15));
     }
     adapter_bounds(offsets, n, M, adapter, first, last, err);

@@ -98,9 +98,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     if (kept) {
         if (warp == 0) {
             int padded = 0;
+            bool in_order = true;  // every pair before these 32
             for (int a0 = 0; a0 < g.n; a0 += 32) {
                 int first = 0, last = 0;
-                if (a0 + lane < g.n) adapter_bounds(g.offsets, g.n, g.M, a0 + lane, first, last, err);
+                const bool pair = a0 + lane >= g.n || adapter_bounds(g.offsets, g.n, g.M, a0 + lane, first, last, err);
+                const unsigned bad = __ballot_sync(0xFFFFFFFFu, !pair);
+                if (!in_order || (bad != 0u && lane >= __ffs(bad) - 1)) first = last = 0;
+                in_order = in_order && bad == 0u;
                 const int rows16 = (last - first + 15) & ~15;
                 int upto = rows16;
 #pragma unroll

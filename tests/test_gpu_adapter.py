@@ -225,6 +225,28 @@ def test_adapter_bad_lists_are_reported(M, width):
     nq().sync_status()
 
 
+@pytest.mark.parametrize("M,n", [(60, 5), (300, 5), (300, 40), (300, 700), (300, 1500)])
+def test_adapter_offsets_whose_groups_overlap(M, n):
+    """Offsets that are each within 0..M but not in order (0, M, 0, M, ...): the first group counts, what
+    follows is empty, and nothing is written behind the workspace."""
+    need_gpu()
+    c = _make(M, 64, 72, 16, n, ids=torch.zeros(M, dtype=torch.int32, device="cuda"))
+    ad, groups, t, out, back = _run(c)
+    off = torch.tensor([M * (i % 2) for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    bad = nq().AdapterRows(groups.rows, off)
+    need = ad.workspace_bytes(M)
+    ws = torch.full((need + 4096 * n,), 0x5A, dtype=torch.uint8, device="cuda")
+    t2 = torch.zeros_like(t)
+    got = nq().adapter_forward(ad, bad, c["x"], c["y"], t=t2)
+    grads = nq().adapter_backward(ad, bad, c["x"], c["ybar"], t, c["xbar"], ws=ws)
+    with pytest.raises(nq().NQError) as e:
+        nq().sync_status()
+    assert e.value.status == 10
+    assert (ws[need:] == 0x5A).all()
+    assert torch.equal(got, out) and torch.equal(t2, t)
+    assert torch.equal(grads[0], back[0]) and torch.equal(grads[1][0], back[1][0]) and torch.equal(grads[2][0], back[2][0])
+
+
 def test_adapter_repeats_on_other_streams_and_in_graphs():
     need_gpu()
     for M in (24, 600):
