@@ -279,6 +279,7 @@ NQ_API nq_status nq_silu_mul(const uint16_t* g, const uint16_t* u, uint16_t* h, 
  */
 #define NQ_ADAPTER_MAX_RANK 128
 #define NQ_ADAPTER_MAX_N 16384
+#define NQ_ADAPTER_MAX_M 1000000000 /* rows of a batch: the kernels count rows, padded by group, in 32 bits */
 typedef struct nq_adapters {
     int64_t n;           /* adapters */
     int64_t rank;
@@ -297,7 +298,8 @@ typedef struct nq_adapters {
  *   rows [M] int32: the row numbers, adapter 0's first, each group in ascending order, the rows
  *   without an adapter last; offsets [n + 1] int32: adapter a has rows[offsets[a] ..
  *   offsets[a+1]), and rows[offsets[n] .. M) have none.
- * A caller that knows its batch on the host may fill both lists itself.  1 <= M < 2^31.
+ * A caller that knows its batch on the host may fill both lists itself.  1 <= M < 2^31
+ * (nq_adapter_forward and nq_adapter_backward take 1 <= M <= NQ_ADAPTER_MAX_M).
  */
 NQ_API nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32_t* rows, int32_t* offsets,
                                  void* stream);

@@ -33,6 +33,13 @@ struct AdapterArgs {
     int part_ld;
 };
 
+// Rows, list entries and padded rows are 32-bit numbers on the device: a group rounded up to a tile of
+// 128, a step of up to 128 past its end, and a row of the second of two arrays of padded rows (a TMA
+// coordinate) all fit.
+static_assert(int64_t{NQ_ADAPTER_MAX_M} + 256 < INT32_MAX &&
+                  2 * (int64_t{NQ_ADAPTER_MAX_M} + 15 * int64_t{NQ_ADAPTER_MAX_N}) < INT32_MAX,
+              "row numbers in 32 bits");
+
 // Padded rows of M rows in n groups, at most.
 inline int64_t max_padded_rows(int64_t M, int64_t n) { return M + 15 * (n < M ? n : M); }
 

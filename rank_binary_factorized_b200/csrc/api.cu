@@ -448,7 +448,7 @@ nq_status check_adapters(const nq_adapters* S, int64_t M) {
     if (S->d_in < 1 || S->d_out < 1 || S->d_in > kMaxRows || S->d_out > kMaxRows || S->lda < S->d_in ||
         S->ldb < S->rank)
         return NQ_ERR_SHAPE;
-    if (M < 1 || M > kMaxRows) return NQ_ERR_SHAPE;
+    if (M < 1 || M > NQ_ADAPTER_MAX_M) return NQ_ERR_SHAPE;
     if (!aligned16(S->A) || !aligned16(S->B) || (S->scale && !aligned16(S->scale))) return NQ_ERR_ALIGN;
     return NQ_OK;
 }
