@@ -280,6 +280,7 @@ NQ_API nq_status nq_silu_mul(const uint16_t* g, const uint16_t* u, uint16_t* h, 
 #define NQ_ADAPTER_MAX_RANK 128
 #define NQ_ADAPTER_MAX_N 16384
 #define NQ_ADAPTER_MAX_M 1000000000 /* rows of a batch: the kernels count rows, padded by group, in 32 bits */
+#define NQ_ADAPTER_MAX_D 1000000000 /* d_in, d_out: columns, rounded up to a tile, likewise */
 typedef struct nq_adapters {
     int64_t n;           /* adapters */
     int64_t rank;

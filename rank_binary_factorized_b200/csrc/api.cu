@@ -445,8 +445,8 @@ constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 nq_status check_adapters(const nq_adapters* S, int64_t M) {
     if (!S || !S->A || !S->B) return NQ_ERR_NULL;
     if (S->n < 1 || S->n > NQ_ADAPTER_MAX_N || S->rank < 1 || S->rank > NQ_ADAPTER_MAX_RANK) return NQ_ERR_SHAPE;
-    if (S->d_in < 1 || S->d_out < 1 || S->d_in > kMaxRows || S->d_out > kMaxRows || S->lda < S->d_in ||
-        S->ldb < S->rank)
+    if (S->d_in < 1 || S->d_out < 1 || S->d_in > NQ_ADAPTER_MAX_D || S->d_out > NQ_ADAPTER_MAX_D ||
+        S->lda < S->d_in || S->ldb < S->rank)
         return NQ_ERR_SHAPE;
     if (M < 1 || M > NQ_ADAPTER_MAX_M) return NQ_ERR_SHAPE;
     if (!aligned16(S->A) || !aligned16(S->B) || (S->scale && !aligned16(S->scale))) return NQ_ERR_ALIGN;

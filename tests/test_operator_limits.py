@@ -39,3 +39,19 @@ def test_adapter_rows_beyond_the_kernels_32_bit_counts_are_refused(nq, n, rank, 
         assert lib.nq_adapter_forward(ctypes.byref(S), 0x40000, 0x50000, 0x60000, 0x70000, 0x80000, 0, most, None) == DEVICE
     padded = most + 15 * _limit("NQ_ADAPTER_MAX_N")
     assert most + 127 < 2 ** 31 and 2 * padded < 2 ** 31
+
+
+def test_adapter_columns_beyond_the_kernels_32_bit_counts_are_refused(nq):
+    """The last tile of columns below 2^31 does not fit 32 bits when it is rounded up."""
+    most = _limit("NQ_ADAPTER_MAX_D")
+    lib = nq.raw_lib()
+    for d_in, d_out in ((2 ** 31 - 8, 64), (64, 2 ** 31 - 8), (most + 8, 64), (64, most + 8), (most, most)):
+        S = nq.nq_adapters(1, 8, d_in, d_out, 0x10000, d_in, 0x20000, 8, 0)
+        taken = max(d_in, d_out) <= most
+        assert (lib.nq_adapter_workspace_bytes(ctypes.byref(S), 4) > 0) == taken
+        if not taken or not torch.cuda.is_available():
+            want = DEVICE if taken else SHAPE
+            assert lib.nq_adapter_forward(ctypes.byref(S), 0x40000, 0x50000, 0x60000, 0x70000, 0x80000, 0, 4, None) == want
+            assert lib.nq_adapter_backward(ctypes.byref(S), 0x40000, 0x50000, 0x60000, 0x70000, 0x80000, 0x90000, 0xA0000,
+                                           0xB0000, 0xC0000, 4, 0xD0000, 1 << 62, None) == want
+    assert most + 2047 < 2 ** 31
