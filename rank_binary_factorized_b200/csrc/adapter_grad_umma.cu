@@ -10,8 +10,10 @@
 // A work unit is one adapter and 256 columns of x or ybar; the blocks take units in turn.  Warp 0
 // loads 64 tokens at a time (z: TMA boxes where rows follow one another, row gathers where not; rows
 // past the group's last arrive as zeros, so that nothing of another row can reach the sum), warp 1
-// issues the MMAs, warps 2..5 round the accumulators to bf16 and store them.  Where the units are fewer
-// than the multiprocessors, several blocks share the tokens of one and a small kernel adds their sums.
+// issues the MMAs, warps 2..5 round the accumulators to bf16 and store them.  The two parts of u and t have
+// accumulators of their own (an infinity of z must not meet them in one sum): up to rank 64 TMEM then
+// holds two units, above it one.  Where the units are fewer than the multiprocessors, several blocks
+// share the tokens of one and a small kernel adds their sums.
 // Measured (B200): 4096 rows of a 70B gate at rank 64 63 us, 302 MB of x and ybar at 4.8 TB/s, 0.73 of the
 // measured copy rate (and as much again of u and t from L2).
 #include <algorithm>
@@ -35,7 +37,7 @@ struct AdapterWgradArgs {
     int slots;
     uint32_t slot_bytes;
     int panels, r16;
-    uint32_t acc_cols;        // TMEM columns of one accumulator pair
+    uint32_t acc_cols;        // TMEM columns of a unit's two accumulators of one part of u or t
     int splits;               // blocks that share the tokens of a unit
     float* partial;           // splits > 1: [splits] sums of gA [n][rank][d_in], then of gB [n][d_out][rank]
     int64_t split_stride, gb_at;
@@ -85,6 +87,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
+    const uint32_t two = panels == 1;  // units that TMEM has room for, less one
     const int per_adapter = wa.in_tiles + wa.out_tiles;
     const int64_t units = static_cast<int64_t>(per_adapter) * g.n * wa.splits;
     // tokens of split sp of a group, in slots
@@ -251,25 +254,26 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             if (b0 >= b1) continue;  // no tokens: the epilogue writes zeros
             const int e_begin = first + b0 * kWgTok, e_end = min(last, first + b1 * kWgTok);
             const bool me = tc::elect_one();
-            const uint32_t i = acc & 1;
+            const uint32_t i = acc & two;
             if (me) {
                 uint32_t jt = it;
                 int js = s;
-                ok = tc::mbar_wait(acc_empty(i), ((acc >> 1) & 1u) ^ 1u, err);
-                const uint32_t d = tmem + i * wa.acc_cols;
+                ok = tc::mbar_wait(acc_empty(i), ((acc >> two) & 1u) ^ 1u, err);
+                const uint32_t d = tmem + i * 2 * wa.acc_cols;
                 for (int e0 = e_begin; e0 < e_end && ok; e0 += kWgTok, ++jt) {
                     if (!(ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err))) break;
                     tc::tc_fence_after();
                     const int steps = (min(kWgTok, last - e0) + 15) / 16;
                     const uint32_t off = js * (wa.slot_bytes >> 4);
                     for (int kk = 0; kk < steps; ++kk) {
-                        const uint32_t first_step = e0 > e_begin || kk > 0;
+                        const uint32_t adds = e0 > e_begin || kk > 0;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint64_t zd = z_desc + off + half * (2 * kWgPanel >> 4) + kk * 128u;
                             const uint64_t td = t_desc + off + kk * 128u;
-                            tc::mma_f16_ss(d + half * (wa.acc_cols / 2), zd, td, idesc, first_step);
-                            tc::mma_f16_ss(d + half * (wa.acc_cols / 2), zd, td + (panels * kWgPanel >> 4), idesc, 1u);
+                            tc::mma_f16_ss(d + half * (wa.acc_cols / 2), zd, td, idesc, adds);
+                            tc::mma_f16_ss(d + wa.acc_cols + half * (wa.acc_cols / 2), zd, td + (panels * kWgPanel >> 4),
+                                           idesc, adds);
                         }
                     }
                     tc::mma_commit(empty(js));
@@ -302,9 +306,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             group(adapter, first, last);
             share(last - first, sp, b0, b1);
             const bool any = b0 < b1;
-            const uint32_t i = acc & 1;
+            const uint32_t i = acc & two;
             if (any) {
-                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc_full(i), (acc >> 1) & 1u, err));
+                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc_full(i), (acc >> two) & 1u, err));
                 if (!ok) break;
                 tc::tc_fence_after();
                 ++acc;
@@ -314,10 +318,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 for (int c0 = 0; c0 < r16; c0 += 32) {
                     uint32_t v[32];
                     if (any) {
-                        tc::tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + i * wa.acc_cols +
-                                                   half * (wa.acc_cols / 2) + c0,
-                                               v);
+                        uint32_t rest[32];
+                        const uint32_t d = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + i * 2 * wa.acc_cols +
+                                           half * (wa.acc_cols / 2) + c0;
+                        tc::tmem_ld_32x32b_x32(d, v);
+                        tc::tmem_ld_32x32b_x32(d + wa.acc_cols, rest);
                         tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(join_parts(v[j], rest[j]));
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;

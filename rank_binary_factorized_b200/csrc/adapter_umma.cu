@@ -495,10 +495,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     }
                 }
                 uint4 hi, lo;
-                split_bf16(v[0], v[1], hi.x, lo.x);
-                split_bf16(v[2], v[3], hi.y, lo.y);
-                split_bf16(v[4], v[5], hi.z, lo.z);
-                split_bf16(v[6], v[7], hi.w, lo.w);
+                split_bf16_same_sign(v[0], v[1], hi.x, lo.x);
+                split_bf16_same_sign(v[2], v[3], hi.y, lo.y);
+                split_bf16_same_sign(v[4], v[5], hi.z, lo.z);
+                split_bf16_same_sign(v[6], v[7], hi.w, lo.w);
                 uint8_t* at = smem_raw + (t_base - tc::smem_u32(smem_raw)) + (c / 8) * kTokBytes + m * 128 +
                               (((c % 8) ^ (m & 7)) << 4);
                 *reinterpret_cast<uint4*>(at) = hi;
@@ -508,6 +508,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         const int64_t to = (static_cast<int64_t>(t.padded) + m) * a.part_ld + c * 8;
                         const int64_t part = a.part_rows * a.part_ld;
                         if (a.u_parts) {
+                            split_bf16(v[0], v[1], hi.x, lo.x);
+                            split_bf16(v[2], v[3], hi.y, lo.y);
+                            split_bf16(v[4], v[5], hi.z, lo.z);
+                            split_bf16(v[6], v[7], hi.w, lo.w);
                             *reinterpret_cast<uint4*>(a.u_parts + to) = hi;
                             *reinterpret_cast<uint4*>(a.u_parts + part + to) = lo;
                         }
