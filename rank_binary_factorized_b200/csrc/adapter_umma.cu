@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             if (tiles > 0) {
                 ok = ok && tc::mbar_wait(t_full, (tiles & 1u) ^ 1u, err);
                 if (lane == 0) tc::bulk_wait_group_read<0>();
+                tc::fence_proxy_async_smem();  // the writes to the staging tiles before the peers' copies to the inbox
                 epilogue_sync();
                 if (eid < static_cast<int>(cs)) tc::mbar_arrive_cluster(cluster_map(peers_ready, eid));
                 __syncwarp();

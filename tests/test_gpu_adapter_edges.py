@@ -5,6 +5,8 @@ import torch
 
 from tests.gpu_util import need_gpu, nq
 from tests.operator_util import adapter_grad_reference, adapter_reference, check
+from tests.test_gpu_adapter import _make as make_batch
+from tests.test_gpu_adapter import _run as run_and_check
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +62,38 @@ def test_adapter_infinities_as_the_definition_has_them(M, rank, n, whole):
         refs, tols = adapter_grad_reference(c["A"], c["B"], None, c["ids"], c["x"], c["ybar"], t, c["xbar"])
         for name, v, r, e in zip(("xbar", "gA", "gB"), back, refs, tols):
             _same_kind(v, r, e, "%s %s %s" % (where, at, name))
+
+
+def _again(c, ad, groups, t, out, back, times):
+    """The same calls give the same bits."""
+    for _ in range(times):
+        t2 = torch.empty_like(t)
+        assert torch.equal(nq().adapter_forward(ad, groups, c["x"], c["y"], t=t2), out) and torch.equal(t2, t)
+        got = nq().adapter_backward(ad, groups, c["x"], c["ybar"], t, c["xbar"])
+        assert all(torch.equal(p, q) for p, q in zip(got, back))
+    nq().sync_status()
+
+
+# Groups of 129 rows make two tiles each, more than the launch reckons with, so that a cluster of 8, 6, 4, 2 or 1
+# blocks takes a second tile (the hand-over of the inbox, the staging tiles, t's rows and the slots between tiles).
+@pytest.mark.parametrize("groups_of_129", [10, 14, 21, 46, 160])
+@pytest.mark.parametrize("rank", [128, 72, 40])
+@pytest.mark.parametrize("in_order", [True, False])
+def test_adapter_clusters_that_take_several_tiles(groups_of_129, rank, in_order):
+    """rows side by side (TMA boxes and stores) and in any order (row gathers, stores by threads)."""
+    need_gpu()
+    n = groups_of_129
+    ids = torch.arange(n, device="cuda", dtype=torch.int32).repeat_interleave(129)
+    if not in_order:
+        ids = ids[torch.randperm(len(ids), generator=torch.Generator(device="cuda").manual_seed(n), device="cuda")]
+    c = make_batch(len(ids), 264, 328, rank, n, ids=ids)
+    _again(c, *run_and_check(c, "%d groups, rank %d" % (n, rank)), 5)
+
+
+# more tiles than clusters by rows alone, and by ragged groups; more units of the gradients than multiprocessors
+@pytest.mark.parametrize("shape", [(40000, 136, 72, 128, 2), (700, 136, 72, 104, 300), (600, 2056, 4104, 128, 8),
+                                   (600, 2056, 4104, 64, 8)])
+def test_adapter_large_ranks_over_many_tiles(shape):
+    need_gpu()
+    c = make_batch(*shape)
+    _again(c, *run_and_check(c, "%r" % (shape,)), 5)
