@@ -289,6 +289,8 @@ def layer_forward(layer: Layer, x: torch.Tensor, y=None, ws=None, stream=None, a
         raise ValueError("adapters: of %d x %d with groups %s, the layer is %d x %d" %
                          (adapters.d_out, adapters.d_in, "given" if groups is not None else "missing", layer.d_out,
                           layer.d_in))
+    if adapters is not None:
+        _check_adapter_call(adapters, groups, x, y, t)
     y = _forward("nq_layer_forward", layer, x, y, ws, stream)
     return y if adapters is None else adapter_forward(adapters, groups, x, y, out=y, t=t, stream=stream)
 
@@ -581,6 +583,21 @@ def _check_groups(ad: Adapters, groups: AdapterRows) -> None:
     if groups.n != ad.n or groups.rows.device != ad.device:
         raise ValueError("groups: for %d adapters on %s, the call has %d on %s" %
                          (groups.n, groups.rows.device, ad.n, ad.device))
+
+
+def _check_adapter_call(ad: Adapters, groups: AdapterRows, x, y, t) -> None:
+    """What adapter_forward would refuse, before the projection in front of it is queued."""
+    dev, M = ad.device, groups.M
+    _check_groups(ad, groups)
+    ptrs = _rows_ptr(x, "x", _BF16, M, ad.d_in, dev) | groups._rows_ptr | groups._offsets_ptr
+    if y is not None:
+        ptrs |= _rows_ptr(y, "y", _BF16, M, ad.d_out, dev)
+    if t is not None:
+        ptrs |= _rows_ptr(t, "t", torch.float32, M, ad.rank, dev)
+    if ptrs & 15:
+        raise NQError("nq_adapter_forward", 3)
+    if ad.workspace_bytes(M) == 0:
+        raise NQError("nq_adapter_workspace_bytes", 2)
 
 
 def adapter_forward(ad: Adapters, groups: AdapterRows, x: torch.Tensor, y: torch.Tensor, out=None, t=None,
