@@ -334,7 +334,7 @@ NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, c
  *   may each be NULL; t is needed for gB, x for gA.
  * Sums are fp32 in a fixed order; every output is rounded once to bf16.  On the tensor cores t and u
  * enter the second products as the sum of two bf16 values, which keeps 16 of their bits.
- * ws: nq_adapter_workspace_bytes(S, M) bytes (0 for invalid adapters or M).
+ * ws: nq_adapter_workspace_bytes(S, M) bytes on the current device (0 for invalid adapters or M).
  */
 NQ_API size_t nq_adapter_workspace_bytes(const nq_adapters* S, int64_t M);
 NQ_API nq_status nq_adapter_backward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets,
@@ -381,7 +381,7 @@ NQ_API nq_status nq_block_norm_forward(const nq_block_norm* N, const uint16_t* y
  * refused without them (NQ_ERR_NULL; g_w_post without post_norm: NQ_ERR_VALUE).  gh may be gh_out
  * and gy may be gx.  Row gradients are rounded once from fp32; the sums over rows are fp32 within
  * a block of rows and fp64 across blocks, in a fixed order.
- * ws: nq_block_norm_workspace_bytes(N, M) bytes (0 for invalid parameters).
+ * ws: nq_block_norm_workspace_bytes(N, M) bytes on the current device (0 for invalid parameters).
  */
 NQ_API size_t nq_block_norm_workspace_bytes(const nq_block_norm* N, int64_t M);
 NQ_API nq_status nq_block_norm_backward(const nq_block_norm* N, const uint16_t* y, const void* h_out,

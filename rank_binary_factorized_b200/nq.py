@@ -17,6 +17,7 @@ Tensor conventions (device tensors, contiguous):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -463,6 +464,13 @@ def silu_mul(g: torch.Tensor, u: torch.Tensor, h=None, stream=None) -> torch.Ten
     return h
 
 
+def _on(device):
+    """A context in which `device` is the current one (None: whichever is)."""
+    if device is None or device.index == torch._C._cuda_getDevice():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
 class Adapters:
     """The low-rank adapters of one projection: A [n][rank][d_in], B [n][d_out][rank] bf16 (rows may
     be strided), scale [n] fp32 or None (all 1).  Row m with adapter a gets
@@ -495,7 +503,8 @@ class Adapters:
         self._ws = None
 
     def workspace_bytes(self, M: int) -> int:
-        return int(_lib.nq_adapter_workspace_bytes(self._ref, int(M)))
+        with _on(self.device):  # the size goes by the device's multiprocessors
+            return int(_lib.nq_adapter_workspace_bytes(self._ref, int(M)))
 
     def workspace(self, M: int) -> torch.Tensor:
         """A workspace large enough for M rows, cached here and grown on demand.  Every backward
@@ -675,8 +684,9 @@ class BlockNorm:
             self._structs[dtype] = (s, ctypes.byref(s))
         self._ws = {}
 
-    def workspace_bytes(self, M: int) -> int:
-        return int(_lib.nq_block_norm_workspace_bytes(self._structs[torch.float32][1], int(M)))
+    def workspace_bytes(self, M: int, device=None) -> int:
+        with _on(torch.device(device) if device is not None else self.device):  # the size goes by the device's multiprocessors
+            return int(_lib.nq_block_norm_workspace_bytes(self._structs[torch.float32][1], int(M)))
 
     def workspace(self, M: int, device=None) -> torch.Tensor:
         """A workspace large enough for M rows, cached here and grown on demand.  Every backward
@@ -685,8 +695,7 @@ class BlockNorm:
         device = torch.device(device if device is not None else self.device if self.device is not None else "cuda")
         if device.index is None:
             device = torch.device(device.type, torch.cuda.current_device())
-        with torch.cuda.device(device):  # the size goes by the device's multiprocessors
-            need = self.workspace_bytes(M)
+        need = self.workspace_bytes(M, device)
         if need == 0:
             raise NQError("nq_block_norm_workspace_bytes", 2)
         ws = self._ws.get(device)

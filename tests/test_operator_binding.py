@@ -67,3 +67,32 @@ def test_adapted_layer_checks_everything_before_the_projection_runs(nq, monkeypa
         with pytest.raises((ValueError, TypeError, nq.NQError)):
             nq.layer_forward(layer, x, **{"adapters": ad, **kw})
         assert not ran, kw
+
+
+def test_workspace_sizes_are_those_of_the_tensors_device(nq, monkeypatch):
+    """The size of a workspace goes by its device's multiprocessors, so the device of the tensors, not the
+    current one, is asked."""
+    current = [1]
+
+    class on:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", on)
+    asked = types.SimpleNamespace(nq_adapter_workspace_bytes=lambda S, M: 100 + current[0],
+                                  nq_block_norm_workspace_bytes=lambda N, M: 200 + current[0])
+    monkeypatch.setattr(nq, "_lib", asked)
+    norm = nq.BlockNorm(64)
+    assert norm.workspace_bytes(3) == 201  # no vectors: the current device
+    norm.device = torch.device("cuda", 0)
+    assert norm.workspace_bytes(3) == 200 and _adapters(nq).workspace_bytes(3) == 100
+    assert current == [1]
+    current[0] = 0
+    assert norm.workspace_bytes(3) == 200 and _adapters(nq).workspace_bytes(3) == 100
