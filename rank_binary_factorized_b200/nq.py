@@ -471,6 +471,19 @@ def _on(device):
     return torch.cuda.device(device)
 
 
+def _workspace_of(owner, M: int, device, stream) -> torch.Tensor:
+    """The workspace of a call that passes none: the owner's cached one or, in a capture, a new one from the
+    graph's memory, which no later call can replace or share."""
+    with _on(device):
+        need = owner.workspace_bytes(M) if torch.cuda.is_current_stream_capturing() else 0
+        if need == 0:
+            return owner.workspace(M)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
 class Adapters:
     """The low-rank adapters of one projection: A [n][rank][d_in], B [n][d_out][rank] bf16 (rows may
     be strided), scale [n] fp32 or None (all 1).  Row m with adapter a gets
@@ -508,8 +521,9 @@ class Adapters:
 
     def workspace(self, M: int) -> torch.Tensor:
         """A workspace large enough for M rows, cached here and grown on demand.  Every backward
-        call that passes no ``ws`` uses it: calls that may run at the same time on the GPU, and
-        CUDA graphs that may, must each pass their own."""
+        call outside a capture that passes no ``ws`` uses it: calls that may run at the same time on
+        the GPU must each pass their own.  A captured call that passes none gets one that belongs to
+        the graph; one that is passed must outlive the graph (this cache drops the smaller when it grows)."""
         need = self.workspace_bytes(M)
         if need == 0:
             raise NQError("nq_adapter_workspace_bytes", 2)
@@ -657,7 +671,7 @@ def adapter_backward(ad: Adapters, groups: AdapterRows, x, ybar: torch.Tensor, t
     else:
         gA = gB = None
     if ws is None:
-        ws = ad.workspace(M)
+        ws = _workspace_of(ad, M, dev, stream)
     pw = _ws_ptr(ws, dev)
     _call("nq_adapter_backward", _lib.nq_adapter_backward, dev, stream, ad._ref, groups._rows_ptr, groups._offsets_ptr,
           px, pyb, pt, pxb, po, pa, pb, M, pw, ws.numel())
@@ -690,8 +704,9 @@ class BlockNorm:
 
     def workspace(self, M: int, device=None) -> torch.Tensor:
         """A workspace large enough for M rows, cached here and grown on demand.  Every backward
-        call that passes no ``ws`` uses it: calls that may run at the same time on the GPU, and
-        CUDA graphs that may, must each pass their own."""
+        call outside a capture that passes no ``ws`` uses it: calls that may run at the same time on
+        the GPU must each pass their own.  A captured call that passes none gets one that belongs to
+        the graph; one that is passed must outlive the graph (this cache drops the smaller when it grows)."""
         device = torch.device(device if device is not None else self.device if self.device is not None else "cuda")
         if device.index is None:
             device = torch.device(device.type, torch.cuda.current_device())
@@ -792,7 +807,7 @@ def block_norm_backward(norm: BlockNorm, y, h_out: torch.Tensor, gx, gh_out, gat
     else:
         g_gate, pgg = rows(g_gate, "g_gate", _BF16)
     if ws is None:
-        ws = norm.workspace(M, dev)
+        ws = _workspace_of(norm, M, dev, stream)
     pw = _ws_ptr(ws, dev)
     _call("nq_block_norm_backward", _lib.nq_block_norm_backward, dev, stream, params, py, h_out.data_ptr(), pg, ldg, pgx,
           pgo, pgh, pgy, pwp, pwo, pgg, M, pw, ws.numel())

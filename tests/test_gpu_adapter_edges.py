@@ -97,3 +97,74 @@ def test_adapter_large_ranks_over_many_tiles(shape):
     need_gpu()
     c = make_batch(*shape)
     _again(c, *run_and_check(c, "%r" % (shape,)), 5)
+
+
+def test_captured_calls_do_not_depend_on_a_cached_workspace_that_grows():
+    """A captured call that passes no workspace keeps none that a later, larger call would replace: what is then
+    allocated in its place stays as it is when the graph is replayed."""
+    need_gpu()
+    c, large = make_batch(300, 264, 328, 16, 2), make_batch(1200, 264, 328, 16, 2)
+    ad, groups, t, out, back = run_and_check(c)
+    N = nq().BlockNorm(264, w_pre=c["x"][0].clone())
+    want = nq().block_norm_backward(N, None, c["x"], c["xbar"], None)
+    ws, wn = ad.workspace(300), N.workspace(300)
+    sizes = [ws.numel(), wn.numel()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = nq().adapter_backward(ad, groups, c["x"], c["ybar"], t, c["xbar"])
+        gn = nq().block_norm_backward(N, None, c["x"], c["xbar"], None)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, back)) and torch.equal(gn[0], want[0]) and torch.equal(gn[2], want[2])
+    del ws, wn
+    assert ad.workspace(1200).numel() > sizes[0]
+    ad.workspace(1200), N.workspace(12000)  # grown: the old ones are given back
+    theirs = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    for v in got + (gn[0], gn[2]):
+        v.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all((v == 0x5A).all() for v in theirs)
+    assert all(torch.equal(p, q) for p, q in zip(got, back)) and torch.equal(gn[0], want[0]) and torch.equal(gn[2], want[2])
+
+
+def test_two_graphs_without_workspaces_run_at_the_same_time():
+    need_gpu()
+    c = make_batch(2000, 264, 328, 64, 3)
+    ad, groups, t, _, _ = run_and_check(c)
+    N = nq().BlockNorm(264, w_pre=c["x"][0].clone())
+    inputs = [(c["x"], c["ybar"], c["xbar"]), tuple(-2 * c[k].flip(0) for k in ("x", "ybar", "xbar"))]
+    want = [nq().adapter_backward(ad, groups, x, yb, t, xb) + nq().block_norm_backward(N, None, x, xb, None)
+            for x, yb, xb in inputs]
+    graphs, results, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for x, yb, xb in inputs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            results.append([nq().adapter_backward(ad, groups, x, yb, t, xb) + nq().block_norm_backward(N, None, x, xb, None)
+                            for _ in range(8)])
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for one, w in zip(results, want):
+            assert all(torch.equal(p, q) for r in one for p, q in zip(r, w) if q is not None)
+
+
+def test_captured_call_on_a_forked_stream():
+    """A capture that forks to another stream: the workspace is not reused on the first one meanwhile."""
+    need_gpu()
+    c = make_batch(300, 264, 328, 16, 2)
+    ad, groups, t, out, back = run_and_check(c)
+    side, g, M = torch.cuda.Stream(), torch.cuda.CUDAGraph(), 300
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = nq().adapter_backward(ad, groups, c["x"], c["ybar"], t, c["xbar"], stream=side)
+        other = [torch.zeros(ad.workspace_bytes(M), dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, back)) and not any(v.any() for v in other)
