@@ -315,9 +315,10 @@ NQ_API nq_status nq_adapter_rows(const int32_t* ids, int64_t M, int64_t n, int32
  *   left undefined.  A list entry outside 0..M-1 is skipped; from the first two offsets out of order
  *   on, the groups count as empty (their adapters' gradients are undefined).  Both make the next
  *   nq_sync_status return NQ_ERR_INDEX; no memory outside the arguments is touched.
- * Sums are fp32 in a fixed order (run-to-run identical); out is rounded once.  On the tensor cores t
- * enters the second product as the sum of two bf16 values, which keeps 16 of its bits.  Needs no
- * workspace.
+ * Sums are fp32 in a fixed order (run-to-run identical); out is rounded once.  On the tensor cores a
+ * partial sum is cut, not rounded, to fp32 after every 16 terms, and t enters the second product as the sum
+ * of two bf16 values, which keeps 16 of its bits (down to 2^-133); NaN and infinite inputs give what
+ * the definition gives.  Needs no workspace.
  */
 NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, const int32_t* offsets,
                                     const uint16_t* x, const uint16_t* y, uint16_t* out, float* t, int64_t M,
@@ -332,8 +333,8 @@ NQ_API nq_status nq_adapter_forward(const nq_adapters* S, const int32_t* rows, c
  *   xbar_out may be xbar.  t: as nq_adapter_forward wrote it (it includes the scale).  gA and gB
  *   are written whole, zeros for an adapter without rows.  xbar_out (then xbar too), gA and gB
  *   may each be NULL; t is needed for gB, x for gA.
- * Sums are fp32 in a fixed order; every output is rounded once to bf16.  On the tensor cores t and u
- * enter the second products as the sum of two bf16 values, which keeps 16 of their bits.
+ * Sums are fp32 in a fixed order; every output is rounded once to bf16.  On the tensor cores partial sums
+ * are cut and t and u enter the second products as the sum of two bf16 values, as in the forward pass.
  * ws: nq_adapter_workspace_bytes(S, M) bytes on the current device (0 for invalid adapters or M).
  */
 NQ_API size_t nq_adapter_workspace_bytes(const nq_adapters* S, int64_t M);

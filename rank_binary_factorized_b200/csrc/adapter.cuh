@@ -181,8 +181,9 @@ __device__ __forceinline__ int find_group(const int32_t* offsets, int n, int64_t
     return padded;
 }
 
-// Upper bound of the number of tiles for any grouping of M rows into n adapters and "none"
-// (none_per_tile <= rows_per_tile).
+// Tiles of M rows in n adapters and "none": with one tile size an upper bound for any grouping, which a grid
+// without a loop needs.  Where none_per_tile is the smaller, the larger of the two extremes (every row
+// listed, none listed): a mixture can make more, and the clusters loop over them.
 inline int64_t max_adapter_tiles(int64_t M, int64_t n, int rows_per_tile, int none_per_tile) {
     const int64_t groups = n + 1 < M ? n + 1 : M;
     const int64_t listed = (M - groups) / rows_per_tile + groups, none = (M - 1) / none_per_tile + 1;

@@ -27,8 +27,8 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
 }
 
 // The same for products that share an accumulator: the second part has the value's sign and is 0 only of a
-// 0, so that against an infinity the parts agree.  (The first is cut instead of rounded, and the
-// smallest number stands in for a second part of nothing.)
+// 0, so that against an infinity the parts agree.  The first is cut instead of rounded, and the smallest
+// number, 2^-133, stands in for a second part of nothing: off by 2^-16 of the value or 2^-133 at most.
 __device__ __forceinline__ uint32_t second_part(float v) {
     const uint32_t bits = __float_as_uint(v);
     const float first = __uint_as_float(bits & 0xFFFF0000u);

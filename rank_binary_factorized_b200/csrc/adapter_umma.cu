@@ -714,7 +714,7 @@ nq_status nq_launch_adapter_umma(const nq::AdapterArgs& a, bool backward, cudaSt
     // The tiles decide how many blocks share one: as many as a portable cluster has while every
     // tile's cluster is resident at once.  How many there are depends on the lists, which only the
     // device has: M / 128 full ones and, for every other group, one that is not.  Clusters loop
-    // over what a finer grouping adds.  Above 64 ranks only powers of two leave room for three slots.
+    // over what another grouping adds.  Above 64 ranks only powers of two leave room for three slots.
     const int64_t least = (a.M + nq::kTok - 1) / nq::kTok;
     const int64_t most = nq::max_adapter_tiles(a.M, a.n, nq::kTok, nq::kNoneTok);
     const int64_t likely = least + std::min<int64_t>(a.n, a.M) / 2;
