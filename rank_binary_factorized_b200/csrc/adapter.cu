@@ -282,10 +282,10 @@ __device__ __forceinline__ void rows_tile(const AdapterArgs& a, RowsShared& s, u
                 const bool there = m < count && r < R;
                 const int64_t at = (static_cast<int64_t>(s.tile.padded) + m) * a.part_ld + r;
                 auto put = [&](uint16_t* to, float v) {
-                    const uint16_t hi = float_to_bf16_bits(v);
-                    const float h = bf16_bits_to_float(hi);
-                    to[at] = hi;
-                    to[at + part] = float_to_bf16_bits(isinf(h) ? 0.f : v - h);
+                    uint32_t hi, lo;
+                    split_for_sums(a.part_ld, v, 0.f, hi, lo);
+                    to[at] = static_cast<uint16_t>(hi);
+                    to[at + part] = static_cast<uint16_t>(lo);
                 };
                 if (a.u_parts) put(a.u_parts, there ? s.t[m][r] : 0.f);
                 if (a.t_parts) {

@@ -24,13 +24,13 @@ struct AdapterArgs {
     int n, rank;
     unsigned int* err;
     // For the sums over tokens on the tensor cores: u, and t_in [M][rank] fp32, as the sum of two bf16
-    // values, rows in the order of `rows` with every adapter's padded to a multiple of 16 by zeros:
+    // values (split_for_sums), rows in the order of `rows` with every adapter's padded to a multiple of 16 by zeros:
     // part p of padded row i at parts + (p part_rows + i) part_ld.  nullptr: not wanted.
     const float* t_in;
     uint16_t* u_parts;
     uint16_t* t_parts;
     int64_t part_rows;
-    int part_ld;
+    int part_ld;  // 64 or 128
 };
 
 // Rows, list entries and padded rows are 32-bit numbers on the device: a group rounded up to a tile of
@@ -196,6 +196,52 @@ __device__ __forceinline__ int checked_row(const int32_t* rows, int64_t i, int64
     if (r >= 0 && r < M) return r;
     flag_error(err, kErrIndex);
     return -1;
+}
+
+// ------------------------------------------------------------------ fp32 values in two bf16 parts
+// What v's bf16 part leaves of it (nothing of an infinity).
+__device__ __forceinline__ float rest_of(float v, uint32_t part) {
+    const float p = __uint_as_float(part);
+    return isinf(p) ? 0.f : v - p;
+}
+
+// Two fp32 values as the sum of two bf16 values each, for products that keep the parts apart (join_parts).
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(a, b);
+    lo = pack_bf16(rest_of(a, hi << 16), rest_of(b, hi & 0xFFFF0000u));
+}
+
+// A sum over first parts and the same over second parts, which have accumulators of their own.  Against an
+// infinity the second parts, which may be 0 or of the other sign, add up to an infinity or NaN that
+// the value itself does not have; the first parts alone then give its infinity or NaN.
+__device__ __forceinline__ float join_parts(uint32_t hi, uint32_t lo) {
+    const float l = __uint_as_float(lo);
+    return __uint_as_float(hi) + (isfinite(l) ? l : 0.f);
+}
+
+// The same for products that share an accumulator: the second part has the value's sign and is 0 only of a
+// 0, so that against an infinity the parts agree.  The first is cut instead of rounded, which costs one bit
+// of 17, and the smallest number, 2^-133, stands in for a second part of nothing: off by 2^-16 of the
+// value or 2^-133 at most.
+__device__ __forceinline__ uint32_t second_part(float v) {
+    const uint32_t bits = __float_as_uint(v);
+    const float first = __uint_as_float(bits & 0xFFFF0000u);
+    const uint32_t rest = float_to_bf16_bits(v == first ? 0.f : v - first);
+    return (rest & 0x7FFFu) != 0u || v == 0.f ? rest : (bits >> 16 & 0x8000u) | 1u;
+}
+__device__ __forceinline__ void split_bf16_same_sign(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    lo = second_part(a) | second_part(b) << 16;
+}
+
+// The sums over tokens have room in TMEM for two units of work and for accumulators of both parts up to
+// rank 64; above it the parts share them.
+__device__ __forceinline__ bool sums_keep_parts_apart(int part_ld) { return part_ld == 64; }
+__device__ __forceinline__ void split_for_sums(int part_ld, float a, float b, uint32_t& hi, uint32_t& lo) {
+    if (sums_keep_parts_apart(part_ld))
+        split_bf16(a, b, hi, lo);
+    else
+        split_bf16_same_sign(a, b, hi, lo);
 }
 
 }  // namespace nq

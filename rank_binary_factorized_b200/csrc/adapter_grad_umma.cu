@@ -10,10 +10,11 @@
 // A work unit is one adapter and 256 columns of x or ybar; the blocks take units in turn.  Warp 0
 // loads 64 tokens at a time (z: TMA boxes where rows follow one another, row gathers where not; rows
 // past the group's last arrive as zeros, so that nothing of another row can reach the sum), warp 1
-// issues the MMAs, warps 2..5 round the accumulators to bf16 and store them.  The two parts of u and t have
-// accumulators of their own (an infinity of z must not meet them in one sum): up to rank 64 TMEM then
-// holds two units, above it one.  Where the units are fewer than the multiprocessors, several blocks
-// share the tokens of one and a small kernel adds their sums.
+// issues the MMAs, warps 2..5 round the accumulators to bf16 and store them.  TMEM holds two units, so that
+// one is stored while the next is summed; up to rank 64 the two parts of u and t have accumulators of
+// their own, which are cut half as often (at rank 128 that would leave room for one unit: the backward pass
+// of 2500 rows of a 7B gate in three even groups took 92 us so, 84 as it is).  Where the units are fewer than the multiprocessors,
+// several blocks share the tokens of one and a small kernel adds their sums.
 // Measured (B200): 4096 rows of a 70B gate at rank 64 63 us, 302 MB of x and ybar at 4.8 TB/s, 0.73 of the
 // measured copy rate (and as much again of u and t from L2).
 #include <algorithm>
@@ -27,6 +28,7 @@ constexpr int kWgCols = 256;                // columns of z of a unit: two MMA t
 constexpr int kWgTok = 64;                  // tokens of a slot
 constexpr uint32_t kWgPanel = kWgTok * 128; // 64 tokens x 64 bf16
 constexpr int kWgThreads = 192;
+constexpr uint32_t kWgUnitCols = 256;       // TMEM columns of a unit
 constexpr int kWgMaxSlots = 4;
 constexpr int kWgGroups = 1024;             // groups whose bounds are kept in shared memory
 
@@ -37,7 +39,7 @@ struct AdapterWgradArgs {
     int slots;
     uint32_t slot_bytes;
     int panels, r16;
-    uint32_t acc_cols;        // TMEM columns of a unit's two accumulators of one part of u or t
+    uint32_t acc_cols;        // TMEM columns of a unit's two accumulators (of one part of u or t, if apart)
     int splits;               // blocks that share the tokens of a unit
     float* partial;           // splits > 1: [splits] sums of gA [n][rank][d_in], then of gB [n][d_out][rank]
     int64_t split_stride, gb_at;
@@ -87,7 +89,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - tc::smem_u32(smem_raw)));
-    const uint32_t two = panels == 1;  // units that TMEM has room for, less one
+    const bool apart = sums_keep_parts_apart(panels * 64);
+    const uint32_t second = apart ? wa.acc_cols : 0u;  // where the second parts' accumulators are
     const int per_adapter = wa.in_tiles + wa.out_tiles;
     const int64_t units = static_cast<int64_t>(per_adapter) * g.n * wa.splits;
     // tokens of split sp of a group, in slots
@@ -254,12 +257,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             if (b0 >= b1) continue;  // no tokens: the epilogue writes zeros
             const int e_begin = first + b0 * kWgTok, e_end = min(last, first + b1 * kWgTok);
             const bool me = tc::elect_one();
-            const uint32_t i = acc & two;
+            const uint32_t i = acc & 1;
             if (me) {
                 uint32_t jt = it;
                 int js = s;
-                ok = tc::mbar_wait(acc_empty(i), ((acc >> two) & 1u) ^ 1u, err);
-                const uint32_t d = tmem + i * 2 * wa.acc_cols;
+                ok = tc::mbar_wait(acc_empty(i), ((acc >> 1) & 1u) ^ 1u, err);
+                const uint32_t d = tmem + i * kWgUnitCols;
                 for (int e0 = e_begin; e0 < e_end && ok; e0 += kWgTok, ++jt) {
                     if (!(ok = tc::mbar_wait(full(js), (jt / slots) & 1u, err))) break;
                     tc::tc_fence_after();
@@ -272,8 +275,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                             const uint64_t zd = z_desc + off + half * (2 * kWgPanel >> 4) + kk * 128u;
                             const uint64_t td = t_desc + off + kk * 128u;
                             tc::mma_f16_ss(d + half * (wa.acc_cols / 2), zd, td, idesc, adds);
-                            tc::mma_f16_ss(d + wa.acc_cols + half * (wa.acc_cols / 2), zd, td + (panels * kWgPanel >> 4),
-                                           idesc, adds);
+                            tc::mma_f16_ss(d + second + half * (wa.acc_cols / 2), zd, td + (panels * kWgPanel >> 4), idesc,
+                                           apart ? adds : 1u);
                         }
                     }
                     tc::mma_commit(empty(js));
@@ -306,9 +309,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             group(adapter, first, last);
             share(last - first, sp, b0, b1);
             const bool any = b0 < b1;
-            const uint32_t i = acc & two;
+            const uint32_t i = acc & 1;
             if (any) {
-                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc_full(i), (acc >> two) & 1u, err));
+                ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(acc_full(i), (acc >> 1) & 1u, err));
                 if (!ok) break;
                 tc::tc_fence_after();
                 ++acc;
@@ -318,14 +321,18 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 for (int c0 = 0; c0 < r16; c0 += 32) {
                     uint32_t v[32];
                     if (any) {
-                        uint32_t rest[32];
-                        const uint32_t d = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + i * 2 * wa.acc_cols +
+                        const uint32_t d = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + i * kWgUnitCols +
                                            half * (wa.acc_cols / 2) + c0;
                         tc::tmem_ld_32x32b_x32(d, v);
-                        tc::tmem_ld_32x32b_x32(d + wa.acc_cols, rest);
-                        tc::tmem_wait_ld();
+                        if (apart) {
+                            uint32_t rest[32];
+                            tc::tmem_ld_32x32b_x32(d + second, rest);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(join_parts(v[j], rest[j]));
+                            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(join_parts(v[j], rest[j]));
+                        } else {
+                            tc::tmem_wait_ld();
+                        }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;

@@ -4,44 +4,6 @@
 #include "adapter.cuh"
 #include "tc_common.cuh"
 
-namespace nq {
-
-// What v's bf16 part leaves of it (nothing of an infinity).
-__device__ __forceinline__ float rest_of(float v, uint32_t part) {
-    const float p = __uint_as_float(part);
-    return isinf(p) ? 0.f : v - p;
-}
-
-// A sum over first parts and the same over second parts, which have accumulators of their own.  Against an
-// infinity the second parts, which may be 0 or of the other sign, add up to an infinity or NaN that
-// the value itself does not have; the first parts alone then give its infinity or NaN.
-__device__ __forceinline__ float join_parts(uint32_t hi, uint32_t lo) {
-    const float l = __uint_as_float(lo);
-    return __uint_as_float(hi) + (isfinite(l) ? l : 0.f);
-}
-
-// Two fp32 values as the sum of two bf16 values each.
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(a, b);
-    lo = pack_bf16(rest_of(a, hi << 16), rest_of(b, hi & 0xFFFF0000u));
-}
-
-// The same for products that share an accumulator: the second part has the value's sign and is 0 only of a
-// 0, so that against an infinity the parts agree.  The first is cut instead of rounded, and the smallest
-// number, 2^-133, stands in for a second part of nothing: off by 2^-16 of the value or 2^-133 at most.
-__device__ __forceinline__ uint32_t second_part(float v) {
-    const uint32_t bits = __float_as_uint(v);
-    const float first = __uint_as_float(bits & 0xFFFF0000u);
-    const uint32_t rest = float_to_bf16_bits(v == first ? 0.f : v - first);
-    return (rest & 0x7FFFu) != 0u || v == 0.f ? rest : (bits >> 16 & 0x8000u) | 1u;
-}
-__device__ __forceinline__ void split_bf16_same_sign(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-    lo = second_part(a) | second_part(b) << 16;
-}
-
-}  // namespace nq
-
 namespace nq_host {
 
 // bf16 tensor of `dims` dimensions, innermost first, 128-byte swizzle.

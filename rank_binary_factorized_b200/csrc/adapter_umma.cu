@@ -509,10 +509,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         const int64_t to = (static_cast<int64_t>(t.padded) + m) * a.part_ld + c * 8;
                         const int64_t part = a.part_rows * a.part_ld;
                         if (a.u_parts) {
-                            split_bf16(v[0], v[1], hi.x, lo.x);
-                            split_bf16(v[2], v[3], hi.y, lo.y);
-                            split_bf16(v[4], v[5], hi.z, lo.z);
-                            split_bf16(v[6], v[7], hi.w, lo.w);
+                            split_for_sums(a.part_ld, v[0], v[1], hi.x, lo.x);
+                            split_for_sums(a.part_ld, v[2], v[3], hi.y, lo.y);
+                            split_for_sums(a.part_ld, v[4], v[5], hi.z, lo.z);
+                            split_for_sums(a.part_ld, v[6], v[7], hi.w, lo.w);
                             *reinterpret_cast<uint4*>(a.u_parts + to) = hi;
                             *reinterpret_cast<uint4*>(a.u_parts + part + to) = lo;
                         }
@@ -523,10 +523,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                                 v[j] = row >= 0 && row < a.M && c * 8 + j < a.rank
                                            ? a.t_in[static_cast<int64_t>(row) * a.rank + c * 8 + j]
                                            : 0.f;
-                            split_bf16(v[0], v[1], hi.x, lo.x);
-                            split_bf16(v[2], v[3], hi.y, lo.y);
-                            split_bf16(v[4], v[5], hi.z, lo.z);
-                            split_bf16(v[6], v[7], hi.w, lo.w);
+                            split_for_sums(a.part_ld, v[0], v[1], hi.x, lo.x);
+                            split_for_sums(a.part_ld, v[2], v[3], hi.y, lo.y);
+                            split_for_sums(a.part_ld, v[4], v[5], hi.z, lo.z);
+                            split_for_sums(a.part_ld, v[6], v[7], hi.w, lo.w);
                             *reinterpret_cast<uint4*>(a.t_parts + to) = hi;
                             *reinterpret_cast<uint4*>(a.t_parts + part + to) = lo;
                         }
