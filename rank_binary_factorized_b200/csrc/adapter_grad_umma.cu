@@ -10,11 +10,12 @@
 // A work unit is one adapter and 256 columns of x or ybar; the blocks take units in turn.  Warp 0
 // loads 64 tokens at a time (z: TMA boxes where rows follow one another, row gathers where not; rows
 // past the group's last arrive as zeros, so that nothing of another row can reach the sum), warp 1
-// issues the MMAs, warps 2..5 round the accumulators to bf16 and store them.  TMEM holds two units, so that
-// one is stored while the next is summed; up to rank 64 the two parts of u and t have accumulators of
-// their own, which are cut half as often (at rank 128 that would leave room for one unit: the backward pass
-// of 2500 rows of a 7B gate in three even groups took 92 us so, 84 as it is).  Where the units are fewer than the multiprocessors,
-// several blocks share the tokens of one and a small kernel adds their sums.
+// issues the MMAs, warps 2..5 round the accumulators to bf16 and store them.  TMEM holds two units, so
+// that one is stored while the next is summed; up to rank 64 the two parts of u and t have
+// accumulators of their own, which are cut half as often (at rank 128 that would leave room for one
+// unit: the backward pass of 2500 rows of a 7B gate in three even groups took 92 us so, 84 as it is).
+// Where the units are fewer than the multiprocessors, several blocks share the tokens of one and a
+// small kernel adds their sums.
 // Measured (B200): 4096 rows of a 70B gate at rank 64 63 us, 302 MB of x and ybar at 4.8 TB/s, 0.73 of the
 // measured copy rate (and as much again of u and t from L2).
 #include <algorithm>

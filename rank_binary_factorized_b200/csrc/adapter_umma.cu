@@ -17,10 +17,11 @@
 //   (plain remote stores of the same took three times as long); it adds them in rank order, scales,
 //   writes t and sends its rows to every block as the sum of two bf16 values (16 bits of t: rounding
 //   t itself to bf16 would add half a unit of its own to the result), in the layout that the second
-//   product's A operand has.
+//   product's A operand has.  Both parts have t's sign and share the accumulator (accumulators of their
+//   own cost the epilogue 8% at 8192 rows of a 70B gate).
 // - The epilogue adds the accumulator to the tile of base in registers and stores it from a staging tile
 //   of its own, so that a slot is free as soon as it is read.
-// Measured (B200): 8192 rows of a 70B gate (8192 -> 28672) at rank 64 193 us, 1.09 GB at 5.6 TB/s, 0.85 of the
+// Measured (B200): 8192 rows of a 70B gate (8192 -> 28672) at rank 64 198 us, 1.09 GB at 5.5 TB/s, 0.84 of the
 // measured copy rate; 5000 rows of 8192 x 8192 at rank 16 50 us (4.9 TB/s); one tile alone 15 to 20 us
 // (some 4 us to the first tile's data, 3 us between the products).
 #include <algorithm>

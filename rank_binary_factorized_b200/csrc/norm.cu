@@ -888,7 +888,8 @@ int row_threads(int64_t d, int E) { return static_cast<int>((d + 32 * E - 1) / (
 
 constexpr int64_t kRingMaxD = 512 * nq::kRingE;
 
-// Blocks a multiprocessor of the ring kernels: 512 threads with 128 registers each in all.
+// Blocks a multiprocessor of the ring kernels: 512 threads with 128 registers each in all.  Shared memory may
+// hold fewer of them (backward, fp32 residual, gate per row); the others then run after those.
 int ring_blocks_per_sm(int64_t d) { return std::max(1, std::min(16, 512 / row_threads(d, nq::kRingE))); }
 
 // Backward: blocks that share the rows; rows too wide for the ring take two blocks of any size.
